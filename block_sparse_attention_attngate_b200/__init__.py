@@ -16,6 +16,9 @@ _PUBLIC = (
     "kcomp_state_bytes", "alloc_kcomp_state", "prefill_gt", "prefill_gt_workspace_bytes", "select_blocks",
     "sparse_decode", "sparse_decode_auto_split", "sparse_decode_noalloc", "sparse_decode_workspace_bytes", "version",
     "set_wait_limit", "get_wait_limit", "set_debug_flags", "WAIT_LIMIT_MIN", "WAIT_LIMIT_MAX",
+    "DenseShape", "PoolDesc", "QkShape", "RowsDesc", "alloc_dense_workspace", "alloc_norm_workspace", "dense_decode",
+    "dense_decode_workspace_bytes", "norm_workspace_bytes", "page_plan", "page_release", "qk_norm_rope",
+    "qk_norm_rope_backward",
 )
 
 __all__ = list(_PUBLIC)

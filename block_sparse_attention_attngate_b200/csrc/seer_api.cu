@@ -880,3 +880,405 @@ seer_status seer_gate_truth(const seer_dims_t* dims, const void* q, const seer_k
 }
 
 }  // extern "C"
+
+extern "C" {
+
+// ---------------------------------------------------------------- page tables
+
+namespace {
+
+seer_status check_pages(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq) {
+  if (batch < 1 || page_size < 1 || num_pages < 1 || max_pages_per_seq < 1)
+    return fail(SEER_ERR_INVALID_ARG, "batch, page_size, num_pages and max_pages_per_seq must be >= 1");
+  if (batch > seer::kMaxDecodeB) return fail(SEER_ERR_UNSUPPORTED, "batch %d > %d", batch, seer::kMaxDecodeB);
+  if ((int64_t)num_pages * page_size > INT32_MAX)
+    return fail(SEER_ERR_UNSUPPORTED, "num_pages * page_size must be below 2^31");
+  return SEER_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+seer_status seer_page_plan(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                           int32_t max_tokens, const int32_t* seqlens, const int32_t* new_tokens,
+                           int32_t* block_table, const int32_t* free_list, const int32_t* free_count,
+                           int32_t* seqlens_out, int32_t* free_count_out, int32_t* cu_tokens, int32_t* slot_map,
+                           int32_t* positions, int32_t* err_word, void* stream) {
+  seer_status st = check_pages(batch, page_size, num_pages, max_pages_per_seq);
+  if (st != SEER_OK) return st;
+  if (max_tokens < 1) return fail(SEER_ERR_INVALID_ARG, "max_tokens must be >= 1");
+  const void* const ptrs[] = {seqlens,     new_tokens,     block_table, free_list, free_count,
+                              seqlens_out, free_count_out, cu_tokens,   slot_map,  positions};
+  for (const void* p : ptrs) {
+    if (!p) return fail(SEER_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(p)) return fail(SEER_ERR_INVALID_ARG, "pointer not 4-byte aligned");
+  }
+  seer::PageParams p{};
+  p.seqlens = seqlens;
+  p.per_request = new_tokens;
+  p.block_table = block_table;
+  p.free_list = free_list;
+  p.free_count = free_count;
+  p.seqlens_out = seqlens_out;
+  p.free_count_out = free_count_out;
+  p.cu_tokens = cu_tokens;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.B = batch;
+  p.page = page_size;
+  p.num_pages = num_pages;
+  p.width = max_pages_per_seq;
+  p.max_tokens = max_tokens;
+  p.err = err_word;
+  cudaError_t e = seer::launch_page_plan(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page_plan launch");
+  return SEER_OK;
+}
+
+seer_status seer_page_release(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                              const int32_t* seqlens, const int32_t* finished, const int32_t* block_table,
+                              int32_t* free_list, const int32_t* free_count, int32_t* seqlens_out,
+                              int32_t* free_count_out, int32_t* err_word, void* stream) {
+  seer_status st = check_pages(batch, page_size, num_pages, max_pages_per_seq);
+  if (st != SEER_OK) return st;
+  const void* const ptrs[] = {seqlens, finished, block_table, free_list, free_count, seqlens_out, free_count_out};
+  for (const void* p : ptrs) {
+    if (!p) return fail(SEER_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(p)) return fail(SEER_ERR_INVALID_ARG, "pointer not 4-byte aligned");
+  }
+  seer::PageParams p{};
+  p.seqlens = seqlens;
+  p.per_request = finished;
+  p.block_table = const_cast<int32_t*>(block_table);   // read only by the release kernel
+  p.free_out = free_list;
+  p.free_count = free_count;
+  p.seqlens_out = seqlens_out;
+  p.free_count_out = free_count_out;
+  p.B = batch;
+  p.page = page_size;
+  p.num_pages = num_pages;
+  p.width = max_pages_per_seq;
+  p.err = err_word;
+  cudaError_t e = seer::launch_page_release(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "page_release launch");
+  return SEER_OK;
+}
+
+// ---------------------------------------------------------------- per-head norm + rotation
+
+namespace {
+
+constexpr int32_t kMaxNormTokens = 1 << 27;   // three kinds of one token a CTA stay inside the grid limit
+
+seer_status check_qk(const seer_qk_t* s) {
+  if (!s) return fail(SEER_ERR_INVALID_ARG, "shape is NULL");
+  if (s->num_tokens < 0 || s->num_q_heads < 1 || s->num_kv_heads < 1)
+    return fail(SEER_ERR_INVALID_ARG, "num_tokens must be >= 0, num_q_heads and num_kv_heads >= 1");
+  if (s->num_tokens > kMaxNormTokens || s->num_q_heads > 65536 || s->num_kv_heads > 65536)
+    return fail(SEER_ERR_UNSUPPORTED, "num_tokens above 2^27 or more than 65536 heads");
+  if (s->head_dim != 64 && s->head_dim != 128)
+    return fail(SEER_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", s->head_dim);
+  if (s->rope_dim < 0 || s->rope_dim > s->head_dim || s->rope_dim % 16)
+    return fail(SEER_ERR_UNSUPPORTED, "rope_dim %d is not a multiple of 16 in [0, head_dim]", s->rope_dim);
+  if (s->dtype != SEER_BF16 && s->dtype != SEER_FP16 && s->dtype != SEER_FP32)
+    return fail(SEER_ERR_UNSUPPORTED, "dtype %d unknown", s->dtype);
+  if (!(s->rope_base > 0.f) || !isfinite(s->rope_base)) return fail(SEER_ERR_INVALID_ARG, "rope_base must be > 0");
+  if (!(s->eps >= 0.f) || !isfinite(s->eps)) return fail(SEER_ERR_INVALID_ARG, "eps must be >= 0");
+  return SEER_OK;
+}
+
+bool has(const seer_rows_t* r) { return r && r->data; }
+
+// Rows (or a pool's strides) that the kernel reads or writes 16 bytes at a time.
+seer_status check_rows(const seer_qk_t* s, const seer_rows_t* r, const char* name, seer::Rows* out) {
+  *out = seer::Rows{};
+  if (!has(r)) return SEER_OK;
+  const int64_t unit = s->dtype == SEER_FP32 ? 4 : 8;
+  if (!aligned16(r->data)) return fail(SEER_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (r->stride_t < 0 || r->stride_h < 0 || r->stride_t % unit || r->stride_h % unit)
+    return fail(SEER_ERR_INVALID_ARG, "%s strides (t=%lld h=%lld) must be non-negative multiples of 16 bytes", name,
+                (long long)r->stride_t, (long long)r->stride_h);
+  out->data = r->data;
+  out->stride_t = r->stride_t;
+  out->stride_h = r->stride_h;
+  return SEER_OK;
+}
+
+// Rows that are written: distinct (t, h) must be distinct memory.
+seer_status check_written(const seer_qk_t* s, const seer_rows_t* r, int heads, const char* name, seer::Rows* out) {
+  const seer_status st = check_rows(s, r, name, out);
+  if (st != SEER_OK || !has(r)) return st;
+  const int64_t T = s->num_tokens, D = s->head_dim;
+  const bool token_major = (heads == 1 || r->stride_h >= D) && (T <= 1 || r->stride_t >= (heads - 1) * r->stride_h + D);
+  const bool head_major = (T <= 1 || r->stride_t >= D) && (heads == 1 || r->stride_h >= (T - 1) * r->stride_t + D);
+  if (T > 0 && !token_major && !head_major)
+    return fail(SEER_ERR_INVALID_ARG, "%s is written but its rows overlap (strides t=%lld h=%lld)", name,
+                (long long)r->stride_t, (long long)r->stride_h);
+  return SEER_OK;
+}
+
+seer_status check_pool(const seer_qk_t* s, const seer_pool_t* c, const char* name, seer::Pool* out) {
+  *out = seer::Pool{};
+  if (!c || !c->data) return SEER_OK;
+  if (s->dtype == SEER_FP32) return fail(SEER_ERR_UNSUPPORTED, "%s: caches are bf16 or fp16", name);
+  if (!aligned16(c->data)) return fail(SEER_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (c->stride_page < 1 || c->stride_h < 1 || c->stride_t < s->head_dim || c->stride_page % 8 || c->stride_h % 8 ||
+      c->stride_t % 8)
+    return fail(SEER_ERR_INVALID_ARG, "%s strides must be positive multiples of 8 elements, stride_t >= head_dim", name);
+  if (c->num_pages < 1 || c->page_size < 1) return fail(SEER_ERR_INVALID_ARG, "%s num_pages and page_size must be >= 1", name);
+  if (c->num_pages > INT32_MAX / c->page_size)
+    return fail(SEER_ERR_UNSUPPORTED, "%s num_pages * page_size must be below 2^31", name);
+  out->data = c->data;
+  out->stride_page = c->stride_page;
+  out->stride_h = c->stride_h;
+  out->stride_t = c->stride_t;
+  return SEER_OK;
+}
+
+void norm_common(const seer_qk_t* s, seer::NormParams* p) {
+  for (int i = 0; i < s->rope_dim / 2; ++i) p->theta[i] = pow((double)s->rope_base, -2.0 * i / s->rope_dim);
+  p->T = s->num_tokens;
+  p->rope_dim = s->rope_dim;
+  p->eps = s->eps;
+  p->kind[0].heads = s->num_q_heads;
+  p->kind[1].heads = p->kind[2].heads = s->num_kv_heads;
+}
+
+}  // namespace
+
+seer_status seer_qk_norm_rope(const seer_qk_t* shape, const seer_rows_t* q, const seer_rows_t* k,
+                              const seer_rows_t* v, const void* q_weight, const void* k_weight,
+                              const int32_t* positions, const seer_rows_t* q_out, const seer_rows_t* k_out,
+                              const seer_rows_t* q_nope, const seer_rows_t* k_nope, const seer_pool_t* k_cache,
+                              const seer_pool_t* v_cache, const int32_t* slot_map, const int32_t* live_tokens,
+                              int32_t* err_word, void* stream) {
+  seer_status st = check_qk(shape);
+  if (st != SEER_OK) return st;
+  if (shape->num_tokens == 0) return SEER_OK;
+  seer::NormParams p{};
+  norm_common(shape, &p);
+  const int Hq = shape->num_q_heads, H = shape->num_kv_heads;
+  if ((st = check_rows(shape, q, "q", &p.kind[0].x)) != SEER_OK) return st;
+  if ((st = check_rows(shape, k, "k", &p.kind[1].x)) != SEER_OK) return st;
+  if ((st = check_rows(shape, v, "v", &p.kind[2].x)) != SEER_OK) return st;
+  if ((st = check_written(shape, q_out, Hq, "q_out", &p.kind[0].out)) != SEER_OK) return st;
+  if ((st = check_written(shape, k_out, H, "k_out", &p.kind[1].out)) != SEER_OK) return st;
+  if ((st = check_written(shape, q_nope, Hq, "q_nope", &p.kind[0].nope)) != SEER_OK) return st;
+  if ((st = check_written(shape, k_nope, H, "k_nope", &p.kind[1].nope)) != SEER_OK) return st;
+  if ((st = check_pool(shape, k_cache, "k_cache", &p.kind[1].cache)) != SEER_OK) return st;
+  if ((st = check_pool(shape, v_cache, "v_cache", &p.kind[2].cache)) != SEER_OK) return st;
+  p.kind[0].ctas = has(q_out) || has(q_nope);
+  p.kind[1].ctas = has(k_out) || has(k_nope) || p.kind[1].cache.data;
+  p.kind[2].ctas = p.kind[2].cache.data != nullptr;
+  if (!p.kind[0].ctas && !p.kind[1].ctas && !p.kind[2].ctas) return fail(SEER_ERR_INVALID_ARG, "no output");
+  const char* const names[3] = {"q", "k", "v"};
+  for (int i = 0; i < 3; ++i)
+    if (p.kind[i].ctas && !p.kind[i].x.data) return fail(SEER_ERR_INVALID_ARG, "%s is NULL but an output of it is not", names[i]);
+  const void* const outs[] = {p.kind[0].out.data, p.kind[1].out.data, p.kind[0].nope.data, p.kind[1].nope.data,
+                              p.kind[1].cache.data, p.kind[2].cache.data};
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j]) return fail(SEER_ERR_INVALID_ARG, "two outputs share their memory");
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)))
+    return fail(SEER_ERR_INVALID_ARG, "norm weight not 16-byte aligned");
+  p.kind[0].weight = q_weight;
+  p.kind[1].weight = k_weight;
+  if (shape->rope_dim > 0 && !positions) return fail(SEER_ERR_INVALID_ARG, "positions is NULL");
+  if (p.kind[1].cache.data || p.kind[2].cache.data) {
+    if (!slot_map) return fail(SEER_ERR_INVALID_ARG, "slot_map is NULL but a cache is given");
+    const seer_pool_t* a = p.kind[1].cache.data ? k_cache : v_cache;
+    const seer_pool_t* b = p.kind[2].cache.data ? v_cache : k_cache;
+    if (a->page_size != b->page_size || a->num_pages != b->num_pages)
+      return fail(SEER_ERR_INVALID_ARG, "k_cache and v_cache differ in page_size or num_pages");
+    p.page_size = a->page_size;
+    p.slots = (int32_t)(a->num_pages * a->page_size);
+  }
+  p.positions = positions;
+  p.slot_map = slot_map;
+  p.live = live_tokens;
+  p.err = err_word;
+  int dev;
+  DevFacts* df;
+  if ((st = device_facts(&dev, &df)) != SEER_OK) return st;
+  cudaError_t e = seer::launch_norm_rope(p, shape->head_dim, shape->dtype, df->sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope launch");
+  return SEER_OK;
+}
+
+size_t seer_qk_norm_rope_workspace_bytes(int32_t head_dim) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return (size_t)seer::kNormPartials * head_dim * sizeof(float);
+}
+
+seer_status seer_qk_norm_rope_backward(const seer_qk_t* shape, const seer_rows_t* dq_out, const seer_rows_t* dk_out,
+                                       const seer_rows_t* dq_nope, const seer_rows_t* dk_nope, const seer_rows_t* q,
+                                       const seer_rows_t* k, const void* q_weight, const void* k_weight,
+                                       const int32_t* positions, const seer_rows_t* dq, const seer_rows_t* dk,
+                                       float* dq_weight, float* dk_weight, const int32_t* live_tokens,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  seer_status st = check_qk(shape);
+  if (st != SEER_OK) return st;
+  if (shape->num_tokens == 0) {   // no rows: the weight gradients are zero
+    for (float* dw : {dq_weight, dk_weight}) {
+      if (!dw) continue;
+      cudaError_t e = cudaMemsetAsync(dw, 0, shape->head_dim * sizeof(float), static_cast<cudaStream_t>(stream));
+      if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope_backward memset");
+    }
+    return SEER_OK;
+  }
+  seer::NormParams p{};
+  norm_common(shape, &p);
+  struct Side {
+    const seer_rows_t *z, *y, *x, *dx;
+    const void* w;
+    float* dw;
+    const char* names[4];
+  };
+  const Side sides[2] = {{dq_out, dq_nope, q, dq, q_weight, dq_weight, {"dq_out", "dq_nope", "q", "dq"}},
+                         {dk_out, dk_nope, k, dk, k_weight, dk_weight, {"dk_out", "dk_nope", "k", "dk"}}};
+  for (int i = 0; i < 2; ++i) {
+    const Side& s = sides[i];
+    seer::NormKind& kd = p.kind[i];
+    if ((st = check_rows(shape, s.z, s.names[0], &kd.out)) != SEER_OK) return st;
+    if ((st = check_rows(shape, s.y, s.names[1], &kd.nope)) != SEER_OK) return st;
+    if ((st = check_rows(shape, s.x, s.names[2], &kd.x)) != SEER_OK) return st;
+    if ((st = check_written(shape, s.dx, kd.heads, s.names[3], &kd.dx)) != SEER_OK) return st;
+    kd.ctas = kd.dx.data != nullptr;
+    if (!kd.ctas) {
+      if (s.w || s.dw) return fail(SEER_ERR_INVALID_ARG, "%s is NULL but its norm weight or gradient is not", s.names[3]);
+      continue;
+    }
+    if (!kd.out.data && !kd.nope.data)
+      return fail(SEER_ERR_INVALID_ARG, "%s needs %s or %s", s.names[3], s.names[0], s.names[1]);
+    if (s.w && !kd.x.data) return fail(SEER_ERR_INVALID_ARG, "%s is NULL", s.names[2]);
+    if (!s.w != !s.dw) return fail(SEER_ERR_INVALID_ARG, "a norm weight and its gradient go together");
+    if (s.w && !aligned16(s.w)) return fail(SEER_ERR_INVALID_ARG, "norm weight not 16-byte aligned");
+    if (s.dw && !aligned4(s.dw)) return fail(SEER_ERR_INVALID_ARG, "weight gradient not 4-byte aligned");
+    kd.weight = s.w;
+    kd.dw = s.dw;
+    if (shape->rope_dim > 0 && kd.out.data && !positions) return fail(SEER_ERR_INVALID_ARG, "positions is NULL");
+  }
+  if (!p.kind[0].ctas && !p.kind[1].ctas) return fail(SEER_ERR_INVALID_ARG, "no output");
+  if (p.kind[0].dx.data == p.kind[1].dx.data || (dq_weight && dq_weight == dk_weight))
+    return fail(SEER_ERR_INVALID_ARG, "two outputs share their memory");
+  if (dq_weight || dk_weight) {
+    const size_t need = seer_qk_norm_rope_workspace_bytes(shape->head_dim);
+    if (!workspace || !aligned16(workspace)) return fail(SEER_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(SEER_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  }
+  p.positions = positions;
+  p.live = live_tokens;
+  p.partial = static_cast<float*>(workspace);
+  int dev;
+  DevFacts* df;
+  if ((st = device_facts(&dev, &df)) != SEER_OK) return st;
+  cudaError_t e =
+      seer::launch_norm_rope_backward(p, shape->head_dim, shape->dtype, df->sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rope_backward launch");
+  return SEER_OK;
+}
+
+// ---------------------------------------------------------------- dense one-token attention
+
+namespace {
+
+seer_status check_dense(const seer_dense_t* s) {
+  if (!s) return fail(SEER_ERR_INVALID_ARG, "shape is NULL");
+  if (s->batch < 1 || s->num_q_heads < 1 || s->num_kv_heads < 1)
+    return fail(SEER_ERR_INVALID_ARG, "batch, num_q_heads and num_kv_heads must be >= 1");
+  if (s->num_q_heads % s->num_kv_heads != 0)
+    return fail(SEER_ERR_INVALID_ARG, "num_q_heads (%d) is not a multiple of num_kv_heads (%d)", s->num_q_heads,
+                s->num_kv_heads);
+  if (s->num_q_heads / s->num_kv_heads > seer::kDenseMaxGroup)
+    return fail(SEER_ERR_UNSUPPORTED, "group size %d > %d", s->num_q_heads / s->num_kv_heads, seer::kDenseMaxGroup);
+  if (s->head_dim != 64 && s->head_dim != 128)
+    return fail(SEER_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", s->head_dim);
+  if (s->dtype != SEER_BF16 && s->dtype != SEER_FP16) return fail(SEER_ERR_UNSUPPORTED, "dtype %d not bf16 or fp16", s->dtype);
+  if (s->batch > seer::kMaxDecodeB) return fail(SEER_ERR_UNSUPPORTED, "batch %d > %d", s->batch, seer::kMaxDecodeB);
+  if ((int64_t)s->batch * s->num_kv_heads >= (int64_t)1 << 30)
+    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads must be below 2^30");
+  if (s->window < 0) return fail(SEER_ERR_INVALID_ARG, "window must be >= 0 (0 = all tokens)");
+  if (!(s->softmax_scale >= 0.f) || !isfinite(s->softmax_scale))
+    return fail(SEER_ERR_INVALID_ARG, "softmax_scale must be >= 0 (0 = 1/sqrt(head_dim))");
+  return SEER_OK;
+}
+
+// join entries | {m, l} of the pieces | outputs of the pieces (two pieces a range: its first and last sequence)
+size_t dense_layout(const seer_dense_t* s, int ctas, size_t* off_ml, size_t* off_o) {
+  const size_t ranges = seer::dense_ranges(ctas, s->num_kv_heads);
+  const size_t tiles = s->num_q_heads / s->num_kv_heads > 8 ? 2 : 1;   // of eight heads
+  *off_ml = up256(ranges * sizeof(int4));
+  *off_o = *off_ml + up256(2 * ranges * tiles * 4 * sizeof(float4));
+  return *off_o + 2 * ranges * tiles * 8 * s->head_dim * sizeof(float);
+}
+
+// Tokens a sequence can have in the cache.
+int64_t kv_capacity(const seer_dense_t* s, const seer_kv_t* kv) {
+  return kv->layout == SEER_KV_PAGED ? (int64_t)kv->max_pages_per_seq * s->page_size : kv->num_tokens;
+}
+
+}  // namespace
+
+size_t seer_dense_decode_workspace_bytes(const seer_dense_t* shape) {
+  if (check_dense(shape) != SEER_OK) return 0;
+  int dev;
+  DevFacts* df;
+  if (device_facts(&dev, &df) != SEER_OK) return 0;
+  size_t a, b;
+  return dense_layout(shape, df->sms, &a, &b);
+}
+
+seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const seer_kv_t* k, const seer_kv_t* v,
+                              const int32_t* seqlens, void* out, float* lse_out, void* workspace,
+                              size_t workspace_bytes, int32_t* err_word, void* stream) {
+  seer_status st = check_dense(shape);
+  if (st != SEER_OK) return st;
+  seer_dims_t dims{};   // of check_kv: the row width is all it looks at
+  dims.head_dim = shape->head_dim;
+  if ((st = check_kv(&dims, k, "k")) != SEER_OK) return st;
+  if ((st = check_kv(&dims, v, "v")) != SEER_OK) return st;
+  if (!q || !seqlens || !out || !workspace) return fail(SEER_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(lse_out))
+    return fail(SEER_ERR_INVALID_ARG, "pointer not aligned (16 bytes; lse 4 bytes)");
+  const bool paged = k->layout == SEER_KV_PAGED || v->layout == SEER_KV_PAGED;
+  if (paged && shape->page_size < 1) return fail(SEER_ERR_INVALID_ARG, "page_size must be >= 1");
+  const int64_t cap = std::min(kv_capacity(shape, k), kv_capacity(shape, v));
+  if (cap > INT32_MAX - 64 || (int64_t)shape->batch * (cap / 32 + 1) >= (int64_t)1 << 30)
+    return fail(SEER_ERR_UNSUPPORTED, "batch * (cache capacity / 32 + 1) must be below 2^30");
+  int dev;
+  DevFacts* df;
+  if ((st = device_facts(&dev, &df)) != SEER_OK) return st;
+  size_t off_ml, off_o;
+  const size_t need = dense_layout(shape, df->sms, &off_ml, &off_o);
+  if (workspace_bytes < need)
+    return fail(SEER_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  seer::DenseParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse_out;
+  p.k = plain(k);
+  p.v = plain(v);
+  p.seqlens = seqlens;
+  p.B = shape->batch;
+  p.Hq = shape->num_q_heads;
+  p.Hkv = shape->num_kv_heads;
+  p.g = shape->num_q_heads / shape->num_kv_heads;
+  p.window = shape->window;
+  p.page = paged ? shape->page_size : 1;
+  p.cap = (int32_t)cap;
+  const float scale = shape->softmax_scale > 0.f ? shape->softmax_scale : 1.0f / sqrtf((float)shape->head_dim);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.join = reinterpret_cast<int4*>(ws);
+  p.ml_part = reinterpret_cast<float4*>(ws + off_ml);
+  p.o_part = reinterpret_cast<float4*>(ws + off_o);
+  p.by_row = (int64_t)p.B * p.Hkv <= seer::dense_ranges(df->sms, p.Hkv);
+  p.err = err_word;
+  cudaError_t e = seer::launch_dense_decode(p, shape->head_dim, shape->dtype, df->sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "dense_decode launch");
+  return SEER_OK;
+}
+
+}  // extern "C"

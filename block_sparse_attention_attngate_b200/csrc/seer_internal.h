@@ -234,6 +234,86 @@ struct TruthParams {
 cudaError_t launch_gate_truth(const CUtensorMap& tk, const TruthParams& p, int D, int BLK, int sms, cudaStream_t s);
 int truth_chunk_blocks();
 
+// ---------------------------------------------------------------- page tables
+struct PageParams {
+  const int32_t* seqlens;       // [B]
+  const int32_t* per_request;   // [B] plan: tokens to append; release: finished flags
+  int32_t* block_table;         // [B, width]
+  const int32_t* free_list;     // [num_pages] stack (plan reads it)
+  int32_t* free_out;            // [num_pages] the same stack (release pushes)
+  const int32_t* free_count;
+  int32_t* seqlens_out;         // may be seqlens
+  int32_t* free_count_out;      // may be free_count
+  int32_t* cu_tokens;           // [B + 1]
+  int32_t* slot_map;            // [max_tokens]
+  int32_t* positions;           // [max_tokens]
+  int32_t B, page, num_pages, width, max_tokens;
+  int32_t* err;
+};
+cudaError_t launch_page_plan(const PageParams& p, cudaStream_t s);
+cudaError_t launch_page_release(const PageParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------- per-head norm + rotation (+ cache write)
+struct Rows {
+  void* data;
+  int64_t stride_t, stride_h;   // elements
+};
+struct Pool {
+  void* data;
+  int64_t stride_page, stride_h, stride_t;   // elements
+};
+// One kind of row (query, key or value heads) of a norm + rotation launch.
+struct NormKind {
+  Rows x;             // input rows; data null: absent (values: the cache copy's source)
+  Rows out, nope;     // forward: rotated / un-rotated outputs (null: absent); backward: their gradients
+  Rows dx;            // backward: gradient of x (null: the kind is absent)
+  Pool cache;         // forward: rows of slot_map (null: absent)
+  const void* weight; // [D] or null (no norm)
+  float* dw;          // backward: [D] or null
+  int32_t heads;
+  int32_t tile;       // tokens per CTA pass, at most kNormMaxTile
+  int32_t tiles;      // ceil(T / tile)
+  int32_t cta0;       // first CTA of the kind's range
+  int32_t ctas;       // and how many (0: the kind has nothing to do)
+};
+struct NormParams {
+  double theta[kMaxHalfGate];   // base^(-2i / rope_dim), i < rope_dim / 2
+  NormKind kind[3];             // query, key, value (values: cache copy only)
+  const int32_t* positions;
+  const int32_t* slot_map;
+  const int32_t* live;          // device row count or null
+  int32_t T, rope_dim, page_size;
+  int32_t slots;                // token slots of the pools
+  float eps;
+  float* partial;               // backward workspace [kNormPartials][D]
+  int32_t* err;
+};
+constexpr int kNormMaxTile = 16;
+constexpr int kNormPartials = 1024;   // CTAs of the backward pass, at most
+cudaError_t launch_norm_rope(const NormParams& p, int D, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_norm_rope_backward(const NormParams& p, int D, int dtype, int sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- dense one-token attention
+struct DenseParams {
+  const uint16_t* q;            // [B, Hq, D]
+  uint16_t* out;                // [B, Hq, D]
+  float* lse;                   // [B, Hq] or null
+  KvPlain k, v;
+  const int32_t* seqlens;       // [B]
+  int32_t B, Hq, Hkv, g, window, page;
+  int32_t cap;                  // tokens the caches hold per sequence
+  float scale_log2;             // softmax scale * log2(e)
+  int4* join;                   // [entries] {row b * Hkv + h, pieces, first range, 0}; fewer than 2 pieces: nothing to join
+  float4* ml_part;              // [2 * ranges][NT * 4] {m, l, m, l} of a lane's two heads (log2 domain)
+  float4* o_part;               // [2 * ranges][NT * d / 16][32] register order
+  int32_t by_row;               // join entries are indexed by row, else by range
+  int32_t* err;
+};
+constexpr int kDenseMaxGroup = 16;
+constexpr int kDenseUnit = 32;  // tokens per scheduling unit
+int dense_ranges(int ctas, int Hkv);   // (range, KV head) pairs of a launch, at most
+cudaError_t launch_dense_decode(const DenseParams& p, int D, int dtype, int ctas, cudaStream_t s);
+
 // Record `msg` as the text seer_last_error() returns on this thread; returns `status`.
 int set_last_error(int status, const char* msg);
 

@@ -27,6 +27,7 @@ SELECT_TOPK, SELECT_THRESHOLD, SELECT_TOPP = 0, 1, 2
 DEVERR_BLOCK_INDEX, DEVERR_PAGE_INDEX, DEVERR_COUNT, DEVERR_TIMEOUT = 1, 2, 4, 8
 WAIT_LIMIT_MIN, WAIT_LIMIT_MAX = 1000, 100_000_000_000
 DEBUG_STARVE_COPIES = 1
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # seer_dtype
 
 EXPORTED = (
     "seer_kcomp_update", "seer_kcomp_state_bytes", "seer_kcomp_append", "seer_kcomp_state_init", "seer_gate_score",
@@ -34,6 +35,8 @@ EXPORTED = (
     "seer_decode_step", "seer_sparse_decode_auto_split",
     "seer_sparse_decode_workspace_bytes", "seer_sparse_decode", "seer_sparse_decode_noalloc",
     "seer_gate_truth_workspace_bytes", "seer_gate_truth", "seer_prefill_gt_workspace_bytes", "seer_prefill_gt",
+    "seer_page_plan", "seer_page_release", "seer_qk_norm_rope", "seer_qk_norm_rope_workspace_bytes",
+    "seer_qk_norm_rope_backward", "seer_dense_decode_workspace_bytes", "seer_dense_decode",
     "seer_set_wait_limit", "seer_get_wait_limit", "seer_set_debug_flags", "seer_last_error", "seer_version",
 )
 
@@ -57,12 +60,35 @@ class KVDesc(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int32)]
 
 
+class RowsDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class PoolDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_page", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("rope_base", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class DenseShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build it with `python -m block_sparse_attention_attngate_b200.build`")
     lib = ctypes.CDLL(path)
     P, I32, I64, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     DP, KP = ctypes.POINTER(Dims), ctypes.POINTER(KVDesc)
+    RP, CP = ctypes.POINTER(RowsDesc), ctypes.POINTER(PoolDesc)
+    QP, SP = ctypes.POINTER(QkShape), ctypes.POINTER(DenseShape)
     sig = {
         "seer_kcomp_update": (I32, [DP, KP, P, P, P, P, P]),
         "seer_kcomp_state_bytes": (SZ, [DP]),
@@ -83,6 +109,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "seer_gate_truth": (I32, [DP, P, KP, P, P, P, P, SZ, P, P]),
         "seer_prefill_gt_workspace_bytes": (SZ, [DP, I32]),
         "seer_prefill_gt": (I32, [DP, P, I32, KP, KP, P, P, P, P, P, SZ, P, P]),
+        "seer_page_plan": (I32, [I32] * 5 + [P] * 12),
+        "seer_page_release": (I32, [I32] * 4 + [P] * 9),
+        "seer_qk_norm_rope": (I32, [QP, RP, RP, RP, P, P, P, RP, RP, RP, RP, CP, CP, P, P, P, P]),
+        "seer_qk_norm_rope_workspace_bytes": (SZ, [I32]),
+        "seer_qk_norm_rope_backward": (I32, [QP, RP, RP, RP, RP, RP, RP, P, P, P, RP, RP, P, P, P, P, SZ, P]),
+        "seer_dense_decode_workspace_bytes": (SZ, [SP]),
+        "seer_dense_decode": (I32, [SP, P, KP, KP, P, P, P, P, SZ, P, P]),
         "seer_set_wait_limit": (I32, [I64]),
         "seer_get_wait_limit": (I64, []),
         "seer_set_debug_flags": (I32, [I32]),
@@ -175,6 +208,14 @@ def _need(t: torch.Tensor, dtype: torch.dtype, name: str, contiguous: bool = Tru
         raise ValueError(f"{name} must be contiguous")
 
 
+def _need_half(t: torch.Tensor, name: str):
+    """bf16 or fp16, any strides."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float16:
+        _need(t, torch.float16, name, contiguous=False)
+    else:
+        _need(t, torch.bfloat16, name, contiguous=False)
+
+
 @dataclass
 class Shape:
     """Problem shape of one attention layer (mirrors seer_dims_t)."""
@@ -198,35 +239,38 @@ class Shape:
 
 
 class KVCache:
-    """A bf16 K or V cache as the library sees it (contiguous or paged)."""
+    """A K or V cache as the library sees it (contiguous or paged).  bf16; dense_decode takes fp16 ones as well."""
 
-    def __init__(self, desc: KVDesc, keep):
+    def __init__(self, desc: KVDesc, keep, dtype: torch.dtype = torch.bfloat16):
         self.desc = desc
         self._keep = keep
+        self.dtype = dtype
 
     @classmethod
     def contiguous(cls, t: torch.Tensor) -> "KVCache":
         """t: [B, Hkv, T, d] view (any strides with unit-stride head_dim)."""
-        _need(t, torch.bfloat16, "kv cache", contiguous=False)
+        _need_half(t, "kv cache")
         if t.dim() != 4 or t.stride(3) != 1:
             raise ValueError("contiguous KV cache must be a 4-D [B, Hkv, T, d] view with unit-stride d")
         d = KVDesc(KV_CONTIGUOUS, t.data_ptr(), t.stride(0), t.stride(1), t.stride(2), t.shape[2], 0, None, 0)
-        return cls(d, (t,))
+        return cls(d, (t,), t.dtype)
 
     @classmethod
     def paged(cls, pool: torch.Tensor, block_table: torch.Tensor) -> "KVCache":
         """pool: [P, Hkv, block, d]; block_table: int32 [B, max_pages_per_seq]."""
-        _need(pool, torch.bfloat16, "page pool", contiguous=False)
+        _need_half(pool, "page pool")
         _need(block_table, torch.int32, "block_table")
         if pool.dim() != 4 or pool.stride(3) != 1:
             raise ValueError("page pool must be a 4-D [P, Hkv, block, d] view with unit-stride d")
         d = KVDesc(KV_PAGED, pool.data_ptr(), pool.stride(0), pool.stride(1), pool.stride(2), 0, pool.shape[0],
                    block_table.data_ptr(), block_table.shape[1])
-        return cls(d, (pool, block_table))
+        return cls(d, (pool, block_table), pool.dtype)
 
     def check(self, shape: "Shape", name: str):
         """The cache holds the shape's sequences, KV heads and head_dim (the library reads it by
         (b, kv-head, token) from the descriptor's strides, so a smaller view would be read past)."""
+        if self.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {self.dtype}")
         if self.desc.layout == KV_CONTIGUOUS:
             t = self._keep[0]
             if t.shape[0] < shape.batch or t.shape[1] != shape.num_kv_heads or t.shape[3] != shape.head_dim:
@@ -588,6 +632,257 @@ def gate_truth(shape: Shape, q: torch.Tensor, k: KVCache, seqlens: torch.Tensor,
     _check(_lib.seer_gate_truth(ctypes.byref(dims), _ptr(q), ctypes.byref(k.desc), _ptr(seqlens), _ptr(scores),
                                 _ptr(log_scores), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _ptr(err), _stream(stream)))
+
+
+def page_plan(page_size: int, seqlens: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor,
+              free_list: torch.Tensor, free_count: torch.Tensor, cu_tokens: torch.Tensor, slot_map: torch.Tensor,
+              positions: torch.Tensor, seqlens_out: Optional[torch.Tensor] = None,
+              free_count_out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """Pages, slots and positions of the tokens that each sequence is about to append (see seer_page_plan).
+
+    block_table int32 [B, width] and free_list int32 [num_pages] are as the caller keeps them; lengths and the free
+    count are updated in place unless seqlens_out / free_count_out are given.  cu_tokens int32 [B + 1]; slot_map and
+    positions int32 [room], filled with -1 / 0 behind the last token."""
+    B = _page_args(page_size, seqlens, new_tokens, "new_tokens", block_table, free_list, free_count)
+    seqlens_out = seqlens if seqlens_out is None else seqlens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _need_shape(seqlens_out, (B,), "seqlens_out")
+    _need_shape(free_count_out, (1,), "free_count_out")
+    _need_shape(cu_tokens, (B + 1,), "cu_tokens")
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1 or slot_map.numel() < 1:
+        raise ValueError("slot_map must be a 1-D tensor of at least one slot")
+    _need_shape(positions, slot_map.shape, "positions")
+    _need_err(err)
+    for t, name in ((seqlens, "seqlens"), (new_tokens, "new_tokens"), (block_table, "block_table"),
+                    (free_list, "free_list"), (free_count, "free_count"), (seqlens_out, "seqlens_out"),
+                    (free_count_out, "free_count_out"), (cu_tokens, "cu_tokens"), (slot_map, "slot_map"),
+                    (positions, "positions")):
+        _need(t, torch.int32, name)
+    _check(_lib.seer_page_plan(B, int(page_size), free_list.numel(), block_table.shape[1], slot_map.numel(),
+                               _ptr(seqlens), _ptr(new_tokens), _ptr(block_table), _ptr(free_list), _ptr(free_count),
+                               _ptr(seqlens_out), _ptr(free_count_out), _ptr(cu_tokens), _ptr(slot_map),
+                               _ptr(positions), _ptr(err), _stream(stream)))
+
+
+def page_release(page_size: int, seqlens: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor,
+                 free_list: torch.Tensor, free_count: torch.Tensor, seqlens_out: Optional[torch.Tensor] = None,
+                 free_count_out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """Give the pages of sequences with finished != 0 back to the free list and set their lengths to 0 (see
+    seer_page_release); in place unless seqlens_out / free_count_out are given."""
+    B = _page_args(page_size, seqlens, finished, "finished", block_table, free_list, free_count)
+    seqlens_out = seqlens if seqlens_out is None else seqlens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _need_shape(seqlens_out, (B,), "seqlens_out")
+    _need_shape(free_count_out, (1,), "free_count_out")
+    _need_err(err)
+    for t, name in ((seqlens, "seqlens"), (finished, "finished"), (block_table, "block_table"),
+                    (free_list, "free_list"), (free_count, "free_count"), (seqlens_out, "seqlens_out"),
+                    (free_count_out, "free_count_out")):
+        _need(t, torch.int32, name)
+    _check(_lib.seer_page_release(B, int(page_size), free_list.numel(), block_table.shape[1], _ptr(seqlens),
+                                  _ptr(finished), _ptr(block_table), _ptr(free_list), _ptr(free_count),
+                                  _ptr(seqlens_out), _ptr(free_count_out), _ptr(err), _stream(stream)))
+
+
+def _page_args(page_size, seqlens, per_request, name: str, block_table, free_list, free_count) -> int:
+    if not isinstance(seqlens, torch.Tensor) or seqlens.dim() != 1:
+        raise ValueError("seqlens must be a 1-D tensor")
+    B = int(seqlens.shape[0])
+    _need_shape(per_request, (B,), name)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, pages)")
+    if not isinstance(free_list, torch.Tensor) or free_list.dim() != 1:
+        raise ValueError("free_list must be a 1-D tensor of num_pages entries")
+    _need_shape(free_count, (1,), "free_count")
+    return B
+
+
+def _rows(t: Optional[torch.Tensor], T: int, heads: int, d: int, dtype: torch.dtype, name: str):
+    """seer_rows_t of a [T, heads, d] view with unit-stride d (None: absent)."""
+    if t is None:
+        return None
+    _need_shape(t, (T, heads, d), name)
+    _need(t, dtype, name, contiguous=False)
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit-stride channels")
+    # an axis of one element may carry any stride; none of it is used
+    return RowsDesc(t.data_ptr(), t.stride(0) if T > 1 else heads * d, t.stride(1) if heads > 1 else d)
+
+
+def _ref(desc):
+    return None if desc is None else ctypes.byref(desc)
+
+
+def _pool(t: Optional[torch.Tensor], heads: int, d: int, dtype: torch.dtype, name: str):
+    """seer_pool_t of a [pages, heads, page, d] view with unit-stride d (None: absent)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[1] != heads or t.shape[3] != d:
+        got = tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name} must be a [pages, {heads}, page, {d}] view, got {got}")
+    _need(t, dtype, name, contiguous=False)
+    if t.stride(3) != 1:
+        raise ValueError(f"{name} must have unit-stride channels")
+    return PoolDesc(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2), t.shape[0], t.shape[2])
+
+
+def _qk_shape(q, k, rope_base: float, rope_dim: Optional[int], eps: float):
+    """(QkShape, T, Hq, Hkv, d, dtype) of query rows and / or key rows."""
+    for t, name in ((q, "q"), (k, "k")):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 3):
+            raise ValueError(f"{name} must be a [tokens, heads, d] tensor")
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k is needed")
+    if one.dtype not in DTYPES:
+        raise TypeError(f"q and k must be one of {list(DTYPES)}, got {one.dtype}")
+    T, d = int(one.shape[0]), int(one.shape[2])
+    Hq = int(q.shape[1]) if q is not None else int(k.shape[1])
+    Hkv = int(k.shape[1]) if k is not None else Hq
+    rope = d if rope_dim is None else int(rope_dim)
+    return QkShape(T, Hq, Hkv, d, rope, DTYPES[one.dtype], float(rope_base), float(eps)), T, Hq, Hkv, d, one.dtype
+
+
+def _norm_vectors(weights, d: int, dtype: torch.dtype):
+    for t, name in weights:
+        if t is not None:
+            _need_shape(t, (d,), name)
+            _need(t, dtype, name)
+
+
+def _token_args(positions, num_tokens, T: int, need_positions: bool):
+    if positions is None and need_positions:
+        raise ValueError("positions is needed (rope_dim > 0)")
+    if positions is not None:
+        _need_shape(positions, (T,), "positions")
+        _need(positions, torch.int32, "positions")
+    if num_tokens is not None:
+        _need_shape(num_tokens, (1,), "num_tokens")
+        _need(num_tokens, torch.int32, "num_tokens")
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 rope_base: float = 1e6, rope_dim: Optional[int] = None, eps: float = 1e-6,
+                 q_nope: Optional[torch.Tensor] = None, k_nope: Optional[torch.Tensor] = None,
+                 v: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                 v_cache: Optional[torch.Tensor] = None, slot_map: Optional[torch.Tensor] = None,
+                 num_tokens: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of each query / key head, position rotation and cache write in one pass (see seer_qk_norm_rope).
+
+    q [T, Hq, d], k and v [T, Hkv, d]: views with unit-stride d of one type (bf16, fp16 or fp32).  Rotated rows go to
+    q_out / k_out, un-rotated (normalised) ones to q_nope / k_nope, keys and values to the rows slot_map [T] of the
+    pools k_cache / v_cache [pages, Hkv, page, d]; whichever is None is not written.  num_tokens (int32 [1], on the
+    device) cuts the rows to the first so many.  rope_dim defaults to d."""
+    shape, T, Hq, Hkv, d, dt = _qk_shape(q, k, rope_base, rope_dim, eps)
+    rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
+        (q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (q_out, Hq, "q_out"), (k_out, Hkv, "k_out"),
+        (q_nope, Hq, "q_nope"), (k_nope, Hkv, "k_nope"))]
+    pools = [_pool(t, Hkv, d, dt, name) for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"))]
+    _norm_vectors(((q_weight, "q_weight"), (k_weight, "k_weight")), d, dt)
+    _token_args(positions, num_tokens, T, shape.rope_dim > 0)
+    if slot_map is not None:
+        _need_shape(slot_map, (T,), "slot_map")
+        _need(slot_map, torch.int32, "slot_map")
+    elif k_cache is not None or v_cache is not None:
+        raise ValueError("slot_map is needed with a cache")
+    _need_err(err)
+    _check(_lib.seer_qk_norm_rope(ctypes.byref(shape), _ref(rows[0]), _ref(rows[1]), _ref(rows[2]), _ptr(q_weight),
+                                  _ptr(k_weight), _ptr(positions), _ref(rows[3]), _ref(rows[4]), _ref(rows[5]),
+                                  _ref(rows[6]), _ref(pools[0]), _ref(pools[1]), _ptr(slot_map), _ptr(num_tokens),
+                                  _ptr(err), _stream(stream)))
+
+
+def norm_workspace_bytes(head_dim: int) -> int:
+    return int(_lib.seer_qk_norm_rope_workspace_bytes(int(head_dim)))
+
+
+def alloc_norm_workspace(head_dim: int, device=None) -> torch.Tensor:
+    """Workspace of qk_norm_rope_backward (partial weight gradients; no initial value needed)."""
+    return torch.empty(max(norm_workspace_bytes(head_dim), 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                          k: Optional[torch.Tensor], positions: Optional[torch.Tensor], dq: Optional[torch.Tensor],
+                          dk: Optional[torch.Tensor], workspace: Optional[torch.Tensor] = None,
+                          q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                          dq_weight: Optional[torch.Tensor] = None, dk_weight: Optional[torch.Tensor] = None,
+                          rope_base: float = 1e6, rope_dim: Optional[int] = None, eps: float = 1e-6,
+                          dq_nope: Optional[torch.Tensor] = None, dk_nope: Optional[torch.Tensor] = None,
+                          num_tokens: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of qk_norm_rope (see seer_qk_norm_rope_backward): dq / dk of the inputs q / k and fp32 [d] dq_weight /
+    dk_weight, from the gradients of the rotated rows (dq_out, dk_out) and of the un-rotated ones (dq_nope, dk_nope);
+    None: that output had none.  workspace: alloc_norm_workspace(d), needed with norm weights."""
+    shape, T, Hq, Hkv, d, dt = _qk_shape(q if q is not None else dq, k if k is not None else dk, rope_base, rope_dim, eps)
+    rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
+        (dq_out, Hq, "dq_out"), (dk_out, Hkv, "dk_out"), (dq_nope, Hq, "dq_nope"), (dk_nope, Hkv, "dk_nope"),
+        (q, Hq, "q"), (k, Hkv, "k"), (dq, Hq, "dq"), (dk, Hkv, "dk"))]
+    _norm_vectors(((q_weight, "q_weight"), (k_weight, "k_weight")), d, dt)
+    _norm_vectors(((dq_weight, "dq_weight"), (dk_weight, "dk_weight")), d, torch.float32)
+    _token_args(positions, num_tokens, T, shape.rope_dim > 0 and (dq_out is not None or dk_out is not None))
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    _check(_lib.seer_qk_norm_rope_backward(ctypes.byref(shape), *[_ref(r) for r in rows[:6]], _ptr(q_weight),
+                                           _ptr(k_weight), _ptr(positions), _ref(rows[6]), _ref(rows[7]),
+                                           _ptr(dq_weight), _ptr(dk_weight), _ptr(num_tokens), _ptr(workspace),
+                                           0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def dense_decode_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    shape = DenseShape(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), 0, 1, 0, 0.0)
+    return int(_lib.seer_dense_decode_workspace_bytes(ctypes.byref(shape)))
+
+
+def alloc_dense_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """Workspace of dense_decode for the current device (pieces of split rows; no initial value needed)."""
+    n = dense_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def dense_decode(q: torch.Tensor, k: KVCache, v: KVCache, seqlens: torch.Tensor, out: torch.Tensor,
+                 workspace: torch.Tensor, window: int = 0, softmax_scale: float = 0.0,
+                 lse: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """Attention of one new token per sequence over its whole cache, or its last `window` tokens (see
+    seer_dense_decode).  q and out [B, Hq, d]; k and v of the same type (bf16 or fp16), contiguous or paged with
+    pages of any size."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a 3-D [B, Hq, d] tensor")
+    B, Hq, d = (int(x) for x in q.shape)
+    heads, pages = [], []
+    for c, name in ((k, "k"), (v, "v")):
+        t = c._keep[0]
+        if t.dim() != 4 or t.shape[3] != d:
+            raise ValueError(f"{name}: rows of {d} channels are needed, got {tuple(t.shape)}")
+        if c.dtype != q.dtype:
+            raise TypeError(f"{name} must be {q.dtype}, got {c.dtype}")
+        heads.append(int(t.shape[1]))
+        if c.desc.layout == KV_PAGED:
+            pages.append(int(t.shape[2]))
+            if c._keep[1].dim() != 2 or c._keep[1].shape[0] < B:
+                raise ValueError(f"{name}: a block table of {B} rows is needed, got {tuple(c._keep[1].shape)}")
+        elif t.shape[0] < B:
+            raise ValueError(f"{name}: a cache of {B} sequences is needed, got {tuple(t.shape)}")
+    if heads[0] != heads[1]:
+        raise ValueError(f"k has {heads[0]} heads, v {heads[1]}")
+    if len(set(pages)) > 1:
+        raise ValueError(f"k has pages of {pages[0]} tokens, v of {pages[1]}")
+    _need_shape(seqlens, (B,), "seqlens")
+    _need_shape(out, (B, Hq, d), "out")
+    if lse is not None:
+        _need_shape(lse, (B, Hq), "lse")
+    _need_err(err)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {q.dtype}")
+    for t, dt, name in ((q, q.dtype, "q"), (seqlens, torch.int32, "seqlens"), (out, q.dtype, "out"),
+                        (workspace, torch.uint8, "workspace")):
+        _need(t, dt, name)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+    shape = DenseShape(B, Hq, heads[0], d, DTYPES[q.dtype], pages[0] if pages else 1, int(window), float(softmax_scale))
+    _check(_lib.seer_dense_decode(ctypes.byref(shape), _ptr(q), ctypes.byref(k.desc), ctypes.byref(v.desc),
+                                  _ptr(seqlens), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err),
+                                  _stream(stream)))
 
 
 class DecodeStep:

@@ -419,6 +419,203 @@ seer_status seer_prefill_gt(const seer_dims_t* dims, const void* q, int32_t max_
                             void* out, float* lse_out, float* gt, void* workspace,
                             size_t workspace_bytes, int32_t* err_word, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Around the step: page tables, per-head norm + rotation + cache write, dense one-token
+ * attention.  The pages take their results as given; these calls share the conventions above
+ * except where they say otherwise (no gate: any page size, up to 16 query heads per KV head).
+ * ------------------------------------------------------------------------------------------ */
+
+/* Element types of the calls below (the gated decode above is bf16 throughout). */
+typedef enum { SEER_BF16 = 0, SEER_FP16 = 1, SEER_FP32 = 2 } seer_dtype;
+
+/*
+ * seer_page_plan -- block tables and slot maps of a paged cache from request lengths, on the GPU.
+ * The pages have no counterpart (their caches arrive with a block table).
+ *
+ * Request b holds L_b = seqlens[b] tokens in own_b = ceil(L_b / page_size) pages, listed in
+ * block_table[b, 0..own_b), and is about to append n_b = new_tokens[b] >= 0 tokens.  The free pages
+ * are a stack, free_list[0 .. F), F = *free_count.  With a_b = ceil((L_b + n_b) / page_size) - own_b,
+ * A_b = a_0 + .. + a_{b-1} and N_b = n_0 + .. + n_{b-1}:
+ *   block_table[b, own_b + i] = free_list[F - 1 - (A_b + i)]     i < a_b   (other entries untouched)
+ *   *free_count_out = F - sum a_b;   seqlens_out[b] = L_b + n_b
+ *   cu_tokens[b] = N_b for b <= B   (cu_tokens[B] = the number of appended tokens)
+ *   for token j < n_b, row t = N_b + j:  positions[t] = L_b + j,
+ *     slot_map[t] = page * page_size + positions[t] % page_size, page = block_table[b, positions[t] / page_size]
+ *   rows cu_tokens[B] <= t < max_tokens:  slot_map[t] = -1, positions[t] = 0
+ * All or nothing: when a length is negative, a request would need more than max_pages_per_seq
+ * pages, more than max_tokens tokens are appended, F lies outside [0, num_pages] or the free pages
+ * do not suffice, then SEER_DEVERR_COUNT is set, the table and the lengths stay as they are
+ * (seqlens_out = seqlens, *free_count_out = F), cu_tokens is all 0, slot_map all -1, positions all 0.
+ * A page id outside [0, num_pages) in the stack or in a part-filled page's entry sets
+ * SEER_DEVERR_PAGE_INDEX; the table entry (from the stack) and the slots on it become -1.
+ *
+ *   seqlens, new_tokens         device int32 [B]
+ *   block_table                 device int32 [B, max_pages_per_seq], updated
+ *   free_list, free_count       device int32 [num_pages], [1]
+ *   seqlens_out, free_count_out device int32 [B], [1]; may be seqlens / free_count themselves
+ *   cu_tokens                   device int32 [B + 1]
+ *   slot_map, positions         device int32 [max_tokens]
+ *   err_word                    device int32 or NULL
+ * batch <= 4096; num_pages * page_size < 2^31.  Integers need no 16-byte alignment (4 bytes do).
+ * Other buffers must not overlap.  One launch: one CTA, or a cluster of eight when there is much to
+ * write.
+ */
+seer_status seer_page_plan(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                           int32_t max_tokens, const int32_t* seqlens, const int32_t* new_tokens,
+                           int32_t* block_table, const int32_t* free_list, const int32_t* free_count,
+                           int32_t* seqlens_out, int32_t* free_count_out, int32_t* cu_tokens,
+                           int32_t* slot_map, int32_t* positions, int32_t* err_word, void* stream);
+
+/*
+ * seer_page_release -- give the pages of finished requests back (no counterpart in the pages).
+ *
+ * With own_b = ceil(L_b / page_size) for requests whose finished[b] != 0 (0 for the others) and
+ * R_b = own_0 + .. + own_{b-1}:
+ *   free_list[F + R_b + i] = block_table[b, i]   i < own_b
+ *   *free_count_out = F + sum own_b;   seqlens_out[b] = 0 where finished[b] != 0, else L_b
+ * The table is left as it is.  All or nothing as seer_page_plan (a negative length or more than
+ * max_pages_per_seq pages of a finished request, F outside [0, num_pages], or more than num_pages
+ * free pages afterwards: SEER_DEVERR_COUNT and nothing changes).  A page id outside [0, num_pages) is
+ * pushed as -1 and sets SEER_DEVERR_PAGE_INDEX.  A request released twice without a plan in between
+ * has length 0 the second time and gives nothing back.
+ *   seqlens_out, free_count_out may be seqlens / free_count themselves.
+ */
+seer_status seer_page_release(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                              const int32_t* seqlens, const int32_t* finished, const int32_t* block_table,
+                              int32_t* free_list, const int32_t* free_count, int32_t* seqlens_out,
+                              int32_t* free_count_out, int32_t* err_word, void* stream);
+
+/* Rows of per-head vectors: element (t, h, c) at data + t*stride_t + h*stride_h + c (elements;
+ * both strides multiples of 16 bytes).  data NULL: absent. */
+typedef struct {
+  void* data;
+  int64_t stride_t;
+  int64_t stride_h;
+} seer_rows_t;
+
+/* A pool of token slots to write: slot s is element (s / page_size, h, s % page_size, c) at data +
+ * page*stride_page + h*stride_h + (s % page_size)*stride_t + c.  A contiguous cache [B, Hkv, T, d] is a
+ * pool of B pages of T tokens.  num_pages * page_size < 2^31. */
+typedef struct {
+  void* data;
+  int64_t stride_page;
+  int64_t stride_h;
+  int64_t stride_t;
+  int64_t num_pages;
+  int32_t page_size;
+} seer_pool_t;
+
+/* Shape of seer_qk_norm_rope and its backward pass. */
+typedef struct {
+  int32_t num_tokens;   /* rows T (0: nothing is enqueued) */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t rope_dim;     /* channels rotated: a multiple of 16, 0 <= rope_dim <= head_dim (0: none) */
+  int32_t dtype;        /* seer_dtype of every tensor and of the norm weights */
+  float rope_base;
+  float eps;
+} seer_qk_t;
+
+/*
+ * seer_qk_norm_rope -- RMS norm of every query and key head, the position rotation and the cache
+ * write in one pass.  The pages take q, K (rotated, for the attention) and their un-rotated forms
+ * (for the AttnGate and the compression cache, [CP Knowl 1-2]) as given; this call makes both.
+ *
+ * For row t < min(T, *live_tokens) and head h, x = q[t, h] (or k[t, h]), all in fp32:
+ *   y   = x * w / sqrt(mean(x^2) + eps)      (w = q_weight or k_weight; NULL: y = x, no norm)
+ *   z   = y with channels (i, i + rope_dim/2) rotated by positions[t] * rope_base^(-2i / rope_dim)
+ *         (rotate-half pairing, angles reduced in fp64)
+ *   q_out / k_out = z, q_nope / k_nope = y, k_cache[slot_map[t]] = z (keys), v_cache[slot_map[t]] = v[t]
+ * each rounded once from fp32.  Absent outputs are not written; rows at or behind *live_tokens are
+ * neither read nor written.  A slot of -1 is not written; any other slot outside the pool sets
+ * SEER_DEVERR_PAGE_INDEX and is not written.  Slots of live rows must be distinct (else which
+ * row's channels remain is undefined).
+ *
+ *   q, k         rows [T, Hq, d] / [T, Hkv, d] (any strides: views into one packed projection do);
+ *                k.data may be NULL when no key output is asked for, q.data likewise
+ *   v            rows [T, Hkv, d], or NULL without v_cache
+ *   q_weight, k_weight  device [d] or NULL
+ *   positions    device int32 [T]  (negative ones rotate backwards; not read when rope_dim is 0)
+ *   q_out, k_out, q_nope, k_nope   rows or NULL; each may be the very rows of its input (in place)
+ *                and must not overlap any other input or output
+ *   k_cache, v_cache  pools or NULL (bf16 and fp16 only); slot_map device int32 [T]
+ *   live_tokens  device int32 [1] or NULL (all T rows); e.g. cu_tokens + B of seer_page_plan
+ */
+seer_status seer_qk_norm_rope(const seer_qk_t* shape, const seer_rows_t* q, const seer_rows_t* k,
+                              const seer_rows_t* v, const void* q_weight, const void* k_weight,
+                              const int32_t* positions, const seer_rows_t* q_out, const seer_rows_t* k_out,
+                              const seer_rows_t* q_nope, const seer_rows_t* k_nope, const seer_pool_t* k_cache,
+                              const seer_pool_t* v_cache, const int32_t* slot_map, const int32_t* live_tokens,
+                              int32_t* err_word, void* stream);
+
+/*
+ * seer_qk_norm_rope_backward -- gradients of seer_qk_norm_rope (no counterpart in the pages, which
+ * train the gate alone).
+ *
+ * With dz = dq_out (gradient of the rotated rows, or NULL: 0), dy' = dq_nope (of the un-rotated rows, or NULL: 0),
+ * r = 1 / sqrt(mean(x^2) + eps) and R the row's rotation, per row t < min(T, *live_tokens) in fp32:
+ *   dy = R^T dz + dy';   dx = r * (w dy) - x * r^3 * mean(w dy x);   dw = sum_{t, h} dy * x * r
+ * (no norm weights: dx = dy).  dq / dk are rounded once from fp32; rows at or behind *live_tokens are
+ * not written and add nothing.  dw sums run in a fixed order for a given shape and device (no
+ * atomics), so repeated calls agree bit for bit.
+ *
+ *   dq_out, dk_out, dq_nope, dk_nope   gradient rows or NULL (absent); dq needs dq_out or dq_nope
+ *   q, k         the forward pass's inputs; q / k may be NULL together with dq / dk
+ *   dq, dk       rows, written; each may be the very rows of its dq_out / dq_nope (or dk_..)
+ *   dq_weight, dk_weight   device fp32 [d], written (required with the weight, NULL without)
+ *   workspace    device, >= seer_qk_norm_rope_workspace_bytes(head_dim) bytes, 16-byte aligned, no
+ *                initial value needed; calls on one workspace must not overlap on the GPU
+ */
+size_t seer_qk_norm_rope_workspace_bytes(int32_t head_dim);
+seer_status seer_qk_norm_rope_backward(const seer_qk_t* shape, const seer_rows_t* dq_out, const seer_rows_t* dk_out,
+                                       const seer_rows_t* dq_nope, const seer_rows_t* dk_nope, const seer_rows_t* q,
+                                       const seer_rows_t* k, const void* q_weight, const void* k_weight,
+                                       const int32_t* positions, const seer_rows_t* dq, const seer_rows_t* dk,
+                                       float* dq_weight, float* dk_weight, const int32_t* live_tokens,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Shape of seer_dense_decode. */
+typedef struct {
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;  /* Hq = g * Hkv, 1 <= g <= 16 */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t dtype;         /* SEER_BF16 or SEER_FP16: q, out and both caches */
+  int32_t page_size;     /* tokens per page of paged caches (any size >= 1); ignored for contiguous ones */
+  int32_t window;        /* tokens seen, counted from the last one; 0: all */
+  float softmax_scale;   /* 0 selects 1/sqrt(head_dim) */
+} seer_dense_t;
+
+/*
+ * seer_dense_decode -- attention of one new token per sequence over its whole cache, split over the
+ * cache's length and joined: the dense layers beside the gated ones ([CP Knowl 6]'s flash decoding
+ * without the selection).
+ *
+ * For query head i of KV head h, over tokens t in [max(0, L_b - window), L_b) (window 0: [0, L_b)):
+ *   out[b, i] = sum_t softmax_t(scale * q[b, i] . K[b, h, t]) V[b, h, t]
+ *   lse_out[b, i] = log sum_t exp(scale * q[b, i] . K[b, h, t])
+ * L_b <= 0: out = 0, lse = -inf.  Scores, the running maximum and sum and the output are fp32; the
+ * probabilities that weigh V are rounded to the cache's type (the sum is not).  A sequence longer than
+ * its cache (num_tokens, or max_pages_per_seq * page_size) is cut to it and sets SEER_DEVERR_COUNT; a
+ * page id outside the pool leaves its tokens out and sets SEER_DEVERR_PAGE_INDEX.  Rows at or past
+ * L_b and before the window are not used (they may hold anything, NaN included).
+ *
+ *   q, out     device [B, Hq, d] of the shape's type;  lse_out device fp32 [B, Hq] or NULL
+ *   k, v       caches (see seer_kv_t) of the shape's type, contiguous or paged with page_size tokens per
+ *              page (the two may differ in layout and table)
+ *   seqlens    device int32 [B], L_b counting the new token
+ *   workspace  device, >= seer_dense_decode_workspace_bytes(shape) bytes, 16-byte aligned, no initial
+ *              value needed; calls on one workspace must not overlap on the GPU
+ * batch <= 4096, batch * Hkv < 2^30 and batch * (cache capacity / 32 + 1) < 2^30.  Two launches: the split
+ * pass, one wave of warps over equal ranges of the sequences' tokens, and the join of the rows that lie
+ * in several ranges.  Results do not depend on timing (no atomics).
+ */
+size_t seer_dense_decode_workspace_bytes(const seer_dense_t* shape);
+seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const seer_kv_t* k, const seer_kv_t* v,
+                              const int32_t* seqlens, void* out, float* lse_out, void* workspace,
+                              size_t workspace_bytes, int32_t* err_word, void* stream);
+
 /*
  * Bounded waits of the sparse decode (seer_sparse_decode, seer_sparse_decode_noalloc and the
  * decode launch of the two-launch step).  No passage defines these: they are part of the
