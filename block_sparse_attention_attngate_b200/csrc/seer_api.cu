@@ -1036,8 +1036,23 @@ seer_status check_pool(const seer_qk_t* s, const seer_pool_t* c, const char* nam
   return SEER_OK;
 }
 
+// Frequencies of (base, rope_dim); the thread's last set is kept, since 64 powers cost more than the launch.
+void rope_frequencies(float base, int rope_dim, double* theta) {
+  static thread_local struct {
+    float base = 0.f;
+    int dim = 0;
+    double theta[seer::kMaxHalfGate];
+  } last;
+  if (last.base != base || last.dim != rope_dim) {
+    for (int i = 0; i < rope_dim / 2; ++i) last.theta[i] = pow((double)base, -2.0 * i / rope_dim);
+    last.base = base;
+    last.dim = rope_dim;
+  }
+  memcpy(theta, last.theta, rope_dim / 2 * sizeof(double));
+}
+
 void norm_common(const seer_qk_t* s, seer::NormParams* p) {
-  for (int i = 0; i < s->rope_dim / 2; ++i) p->theta[i] = pow((double)s->rope_base, -2.0 * i / s->rope_dim);
+  rope_frequencies(s->rope_base, s->rope_dim, p->theta);
   p->T = s->num_tokens;
   p->rope_dim = s->rope_dim;
   p->eps = s->eps;
