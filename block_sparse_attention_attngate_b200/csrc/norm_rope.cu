@@ -9,9 +9,8 @@
 // Backward, with r = 1 / sqrt(mean(x^2) + eps):
 //   dy = R^T dz + dy',   dx = r (w dy) - x r^3 mean(w dy x),   dw = sum dy x r
 //
-// Bound: HBM -- every input is read once and every output written once; the
-// angles (fp64 products reduced modulo 2 pi, as in the gate) are computed once
-// per token and CTA, not per head.
+// Bound: HBM -- every input is read once and every output written once.  The arithmetic is close behind it, so it
+// is done two channels at a time (f32x2 instructions) and the addresses are stepped, not computed.
 //
 // Layout.  D / 16 lanes share a row, two 8-channel chunks (16 bytes in 16-bit types) each:
 // lane l of a row takes chunks l and l + rope_dim / 16 while those are
@@ -20,22 +19,67 @@
 // row's lanes then read 128 contiguous bytes per load.  Because a lane writes
 // exactly the elements it has read, every output may be its input's rows.
 //
-// A CTA takes a tile of tokens of one kind (query, key or value heads): about
-// rows_per_cta rows, so the three kinds' CTAs cost alike.
+// Work.  A CTA works on one kind of row (query, key, value), so that all it needs to know of the kind is uniform.
+// A pass is 32 / (D / 16) heads of one token.  Warps are independent.  A token's angles (fp64 products, whole
+// turns taken off) are computed by the warp's lanes while the token's first rows are on their way, exchanged
+// through the warp's own shared memory and kept in registers for all its heads.
+// Forward, a warp takes up to kUnitPasses passes of one token and ends; its rows, position, slot and the live count are
+// all requested at once.  Backward, warps stay (the weight gradients are sums over tokens): each takes an equal run
+// of the list of all passes and keeps passes in flight through a ring in shared memory (cp.async; every lane
+// reads back what it has requested itself, so no lane waits for another).
 #include "seer_device.cuh"
 #include "seer_internal.h"
 
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace seer {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBackwardCtas = 2;   // per SM
 
+// ---------------------------------------------------------------- two channels at a time
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// ---------------------------------------------------------------- chunks of eight channels
 template <typename T>
-struct Chunk {   // eight channels as stored
+struct Chunk {   // as stored
   uint4 v[sizeof(T) == 4 ? 2 : 1];
 };
 
@@ -53,55 +97,49 @@ __device__ __forceinline__ void store_chunk(T* p, const Chunk<T>& c) {
   for (int i = 0; i < (int)(sizeof(c.v) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = c.v[i];
 }
 
-__device__ __forceinline__ void unpack(const Chunk<float>& c, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(c.v[i].x);
-    f[4 * i + 1] = __uint_as_float(c.v[i].y);
-    f[4 * i + 2] = __uint_as_float(c.v[i].z);
-    f[4 * i + 3] = __uint_as_float(c.v[i].w);
-  }
+__device__ __forceinline__ F2 unpack2(uint32_t w, __nv_bfloat16) { return f2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ F2 unpack2(uint32_t w, __half) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2(x.x, x.y);
 }
-__device__ __forceinline__ void unpack(const Chunk<__nv_bfloat16>& c, float (&f)[8]) {
-  const uint32_t w[4] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w};
+template <typename T>
+__device__ __forceinline__ void unpack(const Chunk<T>& c, F2 (&f)[4]) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-__device__ __forceinline__ void unpack(const Chunk<__half>& c, float (&f)[8]) {
-  const uint32_t w[4] = {c.v[0].x, c.v[0].y, c.v[0].z, c.v[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = x.x;
-    f[2 * i + 1] = x.y;
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = f2(__uint_as_float(c.v[i].x), __uint_as_float(c.v[i].y));
+      f[2 * i + 1] = f2(__uint_as_float(c.v[i].z), __uint_as_float(c.v[i].w));
+    }
+  } else {
+    f[0] = unpack2(c.v[0].x, T());
+    f[1] = unpack2(c.v[0].y, T());
+    f[2] = unpack2(c.v[0].z, T());
+    f[3] = unpack2(c.v[0].w, T());
   }
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) { return pack_bf16(a, b); }
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 a, __nv_bfloat16) { return pack_bf16(a.x, a.y); }
+__device__ __forceinline__ uint32_t pack2(float2 a, __half) {
+  const __half2 h = __floats2half2_rn(a.x, a.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <typename T>
-__device__ __forceinline__ Chunk<T> pack(const float (&f)[8]) {
+__device__ __forceinline__ Chunk<T> pack(const F2 (&f)[4]) {
   Chunk<T> c;
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      c.v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                          __float_as_uint(f[4 * i + 3]));
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = split(f[2 * i]), y = split(f[2 * i + 1]);
+      c.v[i] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+    }
   } else {
-    c.v[0] = make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()),
-                        pack2(f[6], f[7], T()));
+    c.v[0] = make_uint4(pack2(split(f[0]), T()), pack2(split(f[1]), T()), pack2(split(f[2]), T()),
+                        pack2(split(f[3]), T()));
   }
   return c;
 }
 
 // The two chunks of lane l (channel offsets) and whether they are a rotated pair.
-template <int D>
 __device__ __forceinline__ bool lane_chunks(int l, int rope_dim, int* c0, int* c1) {
   const int rh = rope_dim >> 4;   // chunks in half of the rotated channels
   const bool rot = l < rh;
@@ -110,33 +148,14 @@ __device__ __forceinline__ bool lane_chunks(int l, int rope_dim, int* c0, int* c
   return rot;
 }
 
-template <typename T>
-__device__ __forceinline__ T* row_at(const Rows& r, int t, int h) {
-  return static_cast<T*>(r.data) + (int64_t)t * r.stride_t + (int64_t)h * r.stride_h;
-}
-
-// cos / sin of the tile's tokens and frequencies: cs[t][i], i < rope_dim / 2.
-__device__ __forceinline__ void tile_angles(const NormParams& p, int t0, int nt, float2* cs) {
-  const int half = p.rope_dim >> 1;
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
-    float c, s;
-    rope_cos_sin((double)p.positions[t0 + t] * p.theta[f], c, s);
-    cs[t * kMaxHalfGate + f] = make_float2(c, s);
-  }
-}
-
-// (a, b) -> (a c - b s, b c + a s), or with the opposite angle
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float2* cs, float sign) {
+// (a, b) -> (a c - b s, b c + a s), or by the opposite angle
+template <bool BACK>
+__device__ __forceinline__ void rotate(F2 (&a)[4], F2 (&b)[4], const F2 (&c)[4], const F2 (&s)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float4 w = *reinterpret_cast<const float4*>(cs + i);   // cos, sin, cos, sin
-    const float s0 = sign * w.y, s1 = sign * w.w;
-    const float a0 = a[i], a1 = a[i + 1];
-    a[i] = a0 * w.x - b[i] * s0;
-    b[i] = b[i] * w.x + a0 * s0;
-    a[i + 1] = a1 * w.z - b[i + 1] * s1;
-    b[i + 1] = b[i + 1] * w.z + a1 * s1;
+  for (int i = 0; i < 4; ++i) {
+    const F2 x = a[i], y = b[i];
+    a[i] = BACK ? fma2(x, c[i], mul2(y, s[i])) : sub2(mul2(x, c[i]), mul2(y, s[i]));
+    b[i] = BACK ? sub2(mul2(y, c[i]), mul2(x, s[i])) : fma2(y, c[i], mul2(x, s[i]));
   }
 }
 
@@ -147,286 +166,446 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ int kind_of(const NormParams& p, int cta) {
-  int k = 0;
-  while (k < 2 && cta >= p.kind[k].cta0 + p.kind[k].ctas) ++k;
-  return k;
-}
-
 __device__ __forceinline__ int live_rows(const NormParams& p) {
   return p.live ? min(max(*p.live, 0), p.T) : p.T;
 }
 
+// Angles of a token, given to each rotated lane as its eight frequencies' cos and sin.
+__device__ __forceinline__ void token_angles(const NormParams& p, int pos, int c0, bool rot, float* cs, F2 (&c)[4],
+                                             F2 (&s)[4]) {
+  const int half = p.rope_dim >> 1;
+  for (int i = threadIdx.x & 31; i < half; i += 32) {
+    const double turns = (double)pos * p.turns[i];
+    float x, y;
+    sincospif((float)(2.0 * (turns - rint(turns))), &y, &x);   // the whole turns go in 64 bits, exactly
+    cs[i] = x;
+    cs[kMaxHalfGate + i] = y;
+  }
+  __syncwarp();
+  if (rot) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(cs + c0 + 4 * i);
+      const float4 y = *reinterpret_cast<const float4*>(cs + kMaxHalfGate + c0 + 4 * i);
+      c[2 * i] = f2(x.x, x.y);
+      c[2 * i + 1] = f2(x.z, x.w);
+      s[2 * i] = f2(y.x, y.y);
+      s[2 * i + 1] = f2(y.z, y.w);
+    }
+  }
+  __syncwarp();   // the next token's angles may go there
+}
+
+template <typename T>
+__device__ __forceinline__ T* lane_row(const Rows& r, int t, int h, int c0) {
+  return static_cast<T*>(r.data) + (int64_t)t * r.stride_t + (int64_t)h * r.stride_h + c0;
+}
+
+// This CTA's kind, and this warp's run of its passes: [first, first + count).
+__device__ __forceinline__ int cta_kind(const NormParams& p) {
+  int k = 0;
+  while (k < 2 && blockIdx.x >= p.kind[k].cta0 + p.kind[k].ctas) ++k;
+  return k;
+}
+__device__ __forceinline__ void warp_run(const NormKind& kd, int live, int batch, int64_t* first, int* count) {
+  const int total = live * kd.passes, W = kd.ctas * kWarps;
+  int run = (total + W - 1) / W;
+  if (run > 2 * batch) run = (run + batch - 1) / batch * batch;
+  *first = (int64_t)((threadIdx.x >> 5) * kd.ctas + (blockIdx.x - kd.cta0)) * run;
+  *count = (int)min((int64_t)run, total - *first);
+}
+
+constexpr int kForwardThreads = 128, kForwardCtas = 5;
+constexpr int kBatch = 4;        // passes requested at once
+constexpr int kUnitPasses = 8;   // of a warp, at most
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormParams p) {
-  constexpr int LPR = D / 16, RPP = kThreads / LPR;   // lanes per row, rows per pass
-  __shared__ __align__(16) float2 cs[kNormMaxTile * kMaxHalfGate];
-  const int which = kind_of(p, blockIdx.x);
+__global__ void __launch_bounds__(kForwardThreads, kForwardCtas) norm_rope_kernel(const __grid_constant__ NormParams p) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;   // lanes per row, rows per pass
+  constexpr int B = sizeof(T) == 4 ? kBatch / 2 : kBatch;
+  __shared__ __align__(16) float angles[kForwardThreads / 32][2 * kMaxHalfGate];
+  const int which = cta_kind(p);
   const NormKind& kd = p.kind[which];
-  const int t0 = (blockIdx.x - kd.cta0) * kd.tile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane & (LPR - 1);
+  const int unit = (blockIdx.x - kd.cta0) * (kForwardThreads / 32) + warp;
+  const int t = unit / kd.units, j = (unit - t * kd.units) * kd.per_unit;
+  if (t >= p.T) return;
+  int c0, c1;
+  const bool rot = lane_chunks(l, p.rope_dim, &c0, &c1);
+  const int gap = c1 - c0;
+  const int n = min(kd.per_unit, kd.passes - j);
+  const int h = j * RPP + sub;
+  int room = kd.heads - h;   // rows h, h + RPP, .. while room > 0
+  const T* src = lane_row<T>(kd.x, t, h, c0);
   pdl_wait();
   pdl_trigger();
-  const int nt = min(kd.tile, live_rows(p) - t0);
-  if (nt <= 0) return;
-  const int rows = nt * kd.heads;
-  const int sub = threadIdx.x / LPR, l = threadIdx.x & (LPR - 1);
-  int c0, c1;
-  const bool rot = lane_chunks<D>(l, p.rope_dim, &c0, &c1) && which < 2;
-
-  Chunk<T> n0 = {}, n1 = {};
-  int nti = 0, nh = 0;
-  auto fetch = [&](int r) {   // the row's chunks, requested one pass ahead
-    if (r < rows) {
-      nti = r / kd.heads;
-      nh = r - nti * kd.heads;
-      const T* x = row_at<T>(kd.x, t0 + nti, nh);
-      n0 = load_chunk(x + c0);
-      n1 = load_chunk(x + c1);
+  Chunk<T> x0[B], x1[B];
+  auto load = [&]() {
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      x0[u] = x1[u] = Chunk<T>{};
+      if (room > u * RPP) {
+        x0[u] = load_chunk(src);
+        x1[u] = load_chunk(src + gap);
+      }
+      src += RPP * kd.x.stride_h;
     }
   };
-  fetch(sub);
-  if (which < 2) tile_angles(p, t0, nt, cs);
-  __syncthreads();
-
-  for (int r0 = 0; r0 < rows; r0 += RPP) {   // uniform over the CTA: the row sums are warp-wide
-    const bool mine = r0 + sub < rows;
-    const Chunk<T> x0 = n0, x1 = n1;
-    const int ti = nti, h = nh;
-    fetch(r0 + RPP + sub);
-    T* dst = nullptr;   // this row's place in the cache
-    if (kd.cache.data != nullptr && mine) {
-      const int slot = p.slot_map[t0 + ti];
-      if (slot >= 0 && slot < p.slots) {
-        const int page = slot / p.page_size;
-        dst = static_cast<T*>(kd.cache.data) + page * kd.cache.stride_page + h * kd.cache.stride_h +
-              (int64_t)(slot - page * p.page_size) * kd.cache.stride_t;
-      } else if (slot != -1 && l == 0) {
-        report(p.err, SEER_DEVERR_PAGE_INDEX);
-      }
+  load();
+  const int live = live_rows(p);
+  const bool turn = which < 2 && p.rope_dim > 0;
+  const int pos = turn ? p.positions[t] : 0;
+  const int slot = kd.cache.data ? p.slot_map[t] : -1;
+  Chunk<T> w0 = {}, w1 = {};
+  if (kd.weight) {
+    w0 = load_chunk(static_cast<const T*>(kd.weight) + c0);
+    w1 = load_chunk(static_cast<const T*>(kd.weight) + c1);
+  }
+  if (t >= live) return;
+  F2 c[4], s[4];
+  if (turn) token_angles(p, pos, c0, rot, angles[warp], c, s);
+  T* cache = nullptr;   // the row's place in the cache
+  if (kd.cache.data) {
+    if (slot >= 0 && slot < p.slots) {
+      const int page = slot / p.page_size;
+      cache = static_cast<T*>(kd.cache.data) + page * kd.cache.stride_page + h * kd.cache.stride_h +
+              (int64_t)(slot - page * p.page_size) * kd.cache.stride_t + c0;
+    } else if (slot != -1 && lane == 0) {
+      report(p.err, SEER_DEVERR_PAGE_INDEX);
     }
-    if (which == 2) {   // values: the cache copy only
-      if (dst) {
-        store_chunk(dst + c0, x0);
-        store_chunk(dst + c1, x1);
-      }
-      continue;
-    }
-    float a[8], b[8];
-    unpack(x0, a);
-    unpack(x1, b);
-    if (kd.weight) {
-      float ss = 0.f;
+  }
+  T* out = lane_row<T>(kd.out, t, h, c0);
+  T* nope = lane_row<T>(kd.nope, t, h, c0);
+  for (int i = 0; i < n; i += B) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-      const float rs = rsqrtf(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
-      float wa[8], wb[8];
-      unpack(load_chunk(static_cast<const T*>(kd.weight) + c0), wa);
-      unpack(load_chunk(static_cast<const T*>(kd.weight) + c1), wb);
+    for (int u = 0; u < B; ++u) {
+      if (i + u >= n) break;
+      const bool mine = room > 0;
+      if (which == 2) {   // values: the cache copy only
+        if (cache && mine) {
+          store_chunk(cache, x0[u]);
+          store_chunk(cache + gap, x1[u]);
+        }
+      } else {
+        F2 a[4], b[4];
+        unpack(x0[u], a);
+        unpack(x1[u], b);
+        if (kd.weight) {
+          F2 q = mul2(a[0], a[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= rs * wa[i];
-        b[i] *= rs * wb[i];
+          for (int e = 1; e < 4; ++e) q = fma2(a[e], a[e], q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q = fma2(b[e], b[e], q);
+          const float2 qs = split(q);
+          const float rs = rsqrtf(row_sum<LPR>(qs.x + qs.y) * (1.0f / D) + p.eps);
+          const F2 r2 = f2(rs, rs);
+          F2 wa[4], wb[4];
+          unpack(w0, wa);
+          unpack(w1, wb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = mul2(a[e], mul2(r2, wa[e]));
+            b[e] = mul2(b[e], mul2(r2, wb[e]));
+          }
+        }
+        if (mine) {
+          if (kd.nope.data) {
+            store_chunk(nope, pack<T>(a));
+            store_chunk(nope + gap, pack<T>(b));
+          }
+          if (rot) rotate<false>(a, b, c, s);
+          const Chunk<T> z0 = pack<T>(a), z1 = pack<T>(b);
+          if (kd.out.data) {
+            store_chunk(out, z0);
+            store_chunk(out + gap, z1);
+          }
+          if (cache) {
+            store_chunk(cache, z0);
+            store_chunk(cache + gap, z1);
+          }
+        }
+        out += RPP * kd.out.stride_h;
+        nope += RPP * kd.nope.stride_h;
       }
+      cache += cache ? RPP * kd.cache.stride_h : 0;
+      room -= RPP;
     }
-    if (!mine) continue;
-    if (kd.nope.data) {
-      T* y = row_at<T>(kd.nope, t0 + ti, h);
-      store_chunk(y + c0, pack<T>(a));
-      store_chunk(y + c1, pack<T>(b));
-    }
-    if (rot) rotate(a, b, cs + ti * kMaxHalfGate + c0, 1.f);
-    const Chunk<T> z0 = pack<T>(a), z1 = pack<T>(b);
-    if (kd.out.data) {
-      T* z = row_at<T>(kd.out, t0 + ti, h);
-      store_chunk(z + c0, z0);
-      store_chunk(z + c1, z1);
-    }
-    if (dst) {
-      store_chunk(dst + c0, z0);
-      store_chunk(dst + c1, z1);
-    }
+    if (i + B < n) load();
   }
 }
 
-// Backward: each CTA walks its kind's tiles with a stride, holding the weight gradient of its
-// 16 channels per lane in registers; at the end the CTA's sum goes to its row of the workspace.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+
+// A ring of STAGES passes of three arrays' chunks (x, gradient of the rotated rows, of the un-rotated ones), a
+// lane's 16 bytes beside its neighbours'.
+template <typename T, int STAGES>
+struct Ring {
+  static constexpr int kHalf = (int)sizeof(Chunk<T>) / 16;   // pieces of a chunk
+  static constexpr int kStage = 3 * 2 * kHalf * 512, kBytes = STAGES * kStage;   // per warp
+  static __device__ __forceinline__ void request(uint32_t at, int array, const char* lo, int gap) {
+#pragma unroll
+    for (int i = 0; i < 2 * kHalf; ++i)
+      cp_async16(at + (array * 2 * kHalf + i) * 512, lo + (i < kHalf ? 0 : gap) + i % kHalf * 16);
+  }
+  static __device__ __forceinline__ void read(uint32_t at, int array, Chunk<T>* x0, Chunk<T>* x1) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      x0->v[i] = lds16(at + (array * 2 * kHalf + i) * 512);
+      x1->v[i] = lds16(at + (array * 2 * kHalf + kHalf + i) * 512);
+    }
+  }
+};
+template <typename T>
+constexpr int backward_stages() { return sizeof(T) == 4 ? 2 : 4; }
+
+// Backward: the weight gradient of a lane's 16 channels stays in registers; at the end the lanes, then the CTA's warps
+// are added up in a fixed order and go to the CTA's row of the workspace.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_backward_kernel(const __grid_constant__ NormParams p) {
-  constexpr int LPR = D / 16, RPP = kThreads / LPR;
-  __shared__ __align__(16) float2 cs[kNormMaxTile * kMaxHalfGate];
-  __shared__ float red[kThreads / 32][D];
-  const int which = kind_of(p, blockIdx.x);
+__global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_kernel(const __grid_constant__ NormParams p) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;
+  constexpr int STAGES = backward_stages<T>();
+  using R = Ring<T, STAGES>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float angles[kWarps][2 * kMaxHalfGate];
+  __shared__ float sums[kWarps][D];
+  const int which = cta_kind(p);
   const NormKind& kd = p.kind[which];
-  const int sub = threadIdx.x / LPR, l = threadIdx.x & (LPR - 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane & (LPR - 1);
+  const uint32_t ring = smem_u32(smem) + warp * R::kBytes + lane * 16;
   int c0, c1;
-  const bool rot = lane_chunks<D>(l, p.rope_dim, &c0, &c1);
-  float dw0[8] = {}, dw1[8] = {};
+  const bool rot = lane_chunks(l, p.rope_dim, &c0, &c1);
+  const int gap = (c1 - c0) * (int)sizeof(T);
   pdl_wait();
   pdl_trigger();
   const int live = live_rows(p);
-  for (int tile = blockIdx.x - kd.cta0; tile < kd.tiles; tile += kd.ctas) {
-    const int t0 = tile * kd.tile, nt = min(kd.tile, live - t0);
-    if (nt <= 0) break;
-    const int rows = nt * kd.heads;
-    __syncthreads();   // the previous tile's angles have been used
-    tile_angles(p, t0, nt, cs);
-    __syncthreads();
-    for (int r0 = 0; r0 < rows; r0 += RPP) {
-      const int r = r0 + sub;
-      const bool mine = r < rows;
-      const int ti = mine ? r / kd.heads : 0, h = mine ? r - ti * kd.heads : 0;
-      float a[8] = {}, b[8] = {}, xa[8] = {}, xb[8] = {};
-      if (mine) {
-        Chunk<T> g0 = {}, g1 = {}, y0 = {}, y1 = {}, x0 = {}, x1 = {};
-        if (kd.weight) {
-          const T* x = row_at<T>(kd.x, t0 + ti, h);
-          x0 = load_chunk(x + c0);
-          x1 = load_chunk(x + c1);
+  int64_t first;
+  int left;
+  warp_run(kd, live, 1, &first, &left);
+  F2 dw0[4] = {}, dw1[4] = {};
+  if (left > 0) {
+    int t = (int)first / kd.passes, j = (int)first - t * kd.passes;
+    const bool turn = kd.out.data && p.rope_dim > 0;
+    int npos = turn ? p.positions[t] : 0;   // of the next token
+    int ahead = left, rt = t, rj = j;       // passes to request, and where
+    const char *sx, *sz, *sy;
+    auto place = [&]() {
+      sx = reinterpret_cast<const char*>(lane_row<T>(kd.x, rt, rj * RPP + sub, c0));
+      sz = reinterpret_cast<const char*>(lane_row<T>(kd.out, rt, rj * RPP + sub, c0));
+      sy = reinterpret_cast<const char*>(lane_row<T>(kd.nope, rt, rj * RPP + sub, c0));
+    };
+    place();
+    auto request = [&](uint32_t at) {
+      if (ahead > 0) {
+        if (rj * RPP + sub < kd.heads) {   // rows that are not there stay unread
+          if (kd.weight) R::request(at, 0, sx, gap);
+          if (kd.out.data) R::request(at, 1, sz, gap);
+          if (kd.nope.data) R::request(at, 2, sy, gap);
         }
-        if (kd.out.data) {
-          const T* g = row_at<T>(kd.out, t0 + ti, h);
-          g0 = load_chunk(g + c0);
-          g1 = load_chunk(g + c1);
+        --ahead;
+        if (++rj == kd.passes) {
+          rj = 0;
+          ++rt;
+          place();
+        } else {
+          sx += RPP * (int)sizeof(T) * kd.x.stride_h;
+          sz += RPP * (int)sizeof(T) * kd.out.stride_h;
+          sy += RPP * (int)sizeof(T) * kd.nope.stride_h;
         }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) request(ring + s * R::kStage);
+    Chunk<T> w0 = {}, w1 = {};
+    if (kd.weight) {
+      w0 = load_chunk(static_cast<const T*>(kd.weight) + c0);
+      w1 = load_chunk(static_cast<const T*>(kd.weight) + c1);
+    }
+    uint32_t at = ring, prev = ring + (STAGES - 1) * R::kStage;
+    F2 c[4], s[4];
+    while (left > 0) {
+      const int n = min(kd.passes - j, left);
+      if (turn) {
+        const int pos = npos;
+        if (t + 1 < live) npos = p.positions[t + 1];
+        token_angles(p, pos, c0, rot, angles[warp], c, s);
+      }
+      int room = kd.heads - j * RPP - sub;
+      T* out = lane_row<T>(kd.dx, t, j * RPP + sub, c0);
+      for (int i = 0; i < n; ++i) {
+        cp_wait<STAGES - 2>();
+        const bool mine = room > 0;
+        Chunk<T> x0 = {}, x1 = {}, z0 = {}, z1 = {}, y0 = {}, y1 = {};
+        if (mine) {
+          if (kd.weight) R::read(at, 0, &x0, &x1);
+          if (kd.out.data) R::read(at, 1, &z0, &z1);
+          if (kd.nope.data) R::read(at, 2, &y0, &y1);
+        }
+        request(prev);
+        prev = at;
+        at = at == ring + (STAGES - 1) * R::kStage ? ring : at + R::kStage;
+        F2 a[4], b[4];
+        unpack(z0, a);
+        unpack(z1, b);
+        if (rot && turn) rotate<true>(a, b, c, s);
         if (kd.nope.data) {
-          const T* g = row_at<T>(kd.nope, t0 + ti, h);
-          y0 = load_chunk(g + c0);
-          y1 = load_chunk(g + c1);
-        }
-        unpack(g0, a);
-        unpack(g1, b);
-        if (rot) rotate(a, b, cs + ti * kMaxHalfGate + c0, -1.f);
-        if (kd.nope.data) {
-          float ya[8], yb[8];
+          F2 ya[4], yb[4];
           unpack(y0, ya);
           unpack(y1, yb);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            a[i] += ya[i];
-            b[i] += yb[i];
+          for (int e = 0; e < 4; ++e) {
+            a[e] = add2(a[e], ya[e]);
+            b[e] = add2(b[e], yb[e]);
           }
         }
-        unpack(x0, xa);
-        unpack(x1, xb);
-      }
-      if (kd.weight) {
-        float wa[8], wb[8];
-        unpack(load_chunk(static_cast<const T*>(kd.weight) + c0), wa);
-        unpack(load_chunk(static_cast<const T*>(kd.weight) + c1), wb);
-        float ss = 0.f, sd = 0.f;
+        if (kd.weight) {
+          F2 ga[4], gb[4], xa[4], xb[4];
+          unpack(x0, xa);
+          unpack(x1, xb);
+          unpack(w0, ga);
+          unpack(w1, gb);
+          F2 q = mul2(xa[0], xa[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss += xa[i] * xa[i] + xb[i] * xb[i];
-          sd += xa[i] * (a[i] * wa[i]) + xb[i] * (b[i] * wb[i]);
-        }
-        const float rs = rsqrtf(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
-        const float k = row_sum<LPR>(sd) * (1.0f / D) * rs * rs;
+          for (int e = 1; e < 4; ++e) q = fma2(xa[e], xa[e], q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw0[i] += a[i] * (xa[i] * rs);
-          dw1[i] += b[i] * (xb[i] * rs);
-          a[i] = rs * (a[i] * wa[i] - xa[i] * k);
-          b[i] = rs * (b[i] * wb[i] - xb[i] * k);
+          for (int e = 0; e < 4; ++e) {
+            q = fma2(xb[e], xb[e], q);
+            ga[e] = mul2(a[e], ga[e]);
+            gb[e] = mul2(b[e], gb[e]);
+          }
+          F2 d = mul2(xa[0], ga[0]);
+#pragma unroll
+          for (int e = 1; e < 4; ++e) d = fma2(xa[e], ga[e], d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d = fma2(xb[e], gb[e], d);
+          const float2 qs = split(q), ds = split(d);
+          const float rs = rsqrtf(row_sum<LPR>(qs.x + qs.y) * (1.0f / D) + p.eps);
+          const float k = row_sum<LPR>(ds.x + ds.y) * (-1.0f / D) * rs * rs;
+          const F2 r2 = f2(rs, rs), k2 = f2(k, k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (mine) {   // an eps of zero makes a row of zeros infinite
+              dw0[e] = fma2(a[e], mul2(xa[e], r2), dw0[e]);
+              dw1[e] = fma2(b[e], mul2(xb[e], r2), dw1[e]);
+            }
+            a[e] = mul2(r2, fma2(xa[e], k2, ga[e]));
+            b[e] = mul2(r2, fma2(xb[e], k2, gb[e]));
+          }
         }
+        if (mine) {
+          store_chunk(out, pack<T>(a));
+          store_chunk(out + (c1 - c0), pack<T>(b));
+        }
+        out += RPP * kd.dx.stride_h;
+        room -= RPP;
       }
-      if (mine) {
-        T* dx = row_at<T>(kd.dx, t0 + ti, h);
-        store_chunk(dx + c0, pack<T>(a));
-        store_chunk(dx + c1, pack<T>(b));
-      }
+      left -= n;
+      j = 0;
+      ++t;
     }
   }
   if (!kd.weight) return;
-  // lanes with the same channels, then the CTA's warps, in a fixed order
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int e = 0; e < 4; ++e) {
+    float2 x = split(dw0[e]), y = split(dw1[e]);
 #pragma unroll
     for (int off = LPR; off < 32; off <<= 1) {
-      dw0[i] += __shfl_xor_sync(0xffffffffu, dw0[i], off);
-      dw1[i] += __shfl_xor_sync(0xffffffffu, dw1[i], off);
+      x.x += __shfl_xor_sync(0xffffffffu, x.x, off);
+      x.y += __shfl_xor_sync(0xffffffffu, x.y, off);
+      y.x += __shfl_xor_sync(0xffffffffu, y.x, off);
+      y.y += __shfl_xor_sync(0xffffffffu, y.y, off);
     }
-  }
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) < LPR) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      red[warp][c0 + i] = dw0[i];
-      red[warp][c1 + i] = dw1[i];
+    if (sub == 0) {
+      *reinterpret_cast<float2*>(&sums[warp][c0 + 2 * e]) = x;
+      *reinterpret_cast<float2*>(&sums[warp][c1 + 2 * e]) = y;
     }
   }
   __syncthreads();
   if (threadIdx.x < D) {
-    float s = 0.f;
+    float x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) s += red[w][threadIdx.x];
-    p.partial[(size_t)blockIdx.x * D + threadIdx.x] = s;
+    for (int w = 0; w < kWarps; ++w) x += sums[w][threadIdx.x];
+    p.partial[(size_t)blockIdx.x * D + threadIdx.x] = x;
   }
 }
 
-// Sum of a kind's partial weight gradients, in a fixed order: CTA 0 the query's, CTA 1 the key's.
-constexpr int kReduceThreads = 1024;
+// Sums of the CTAs' partial weight gradients in a fixed order: 32 channels of one kind a CTA, 32 threads each.
 template <int D>
-__global__ void __launch_bounds__(kReduceThreads) norm_weight_kernel(const __grid_constant__ NormParams p) {
-  constexpr int NG = kReduceThreads / D;
-  __shared__ float red[NG][D];
-  const NormKind& kd = p.kind[blockIdx.x];
-  const int c = threadIdx.x & (D - 1), g = threadIdx.x / D;
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float red[32][33];
+  const int k = blockIdx.x / (D / 32), c = blockIdx.x % (D / 32) * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
+  const NormKind& kd = p.kind[k];
   if (!kd.dw) return;
   float s = 0.f;
 #pragma unroll 8
-  for (int i = g; i < kd.ctas; i += NG) s += p.partial[(size_t)(kd.cta0 + i) * D + c];
-  red[g][c] = s;
+  for (int i = g; i < kd.ctas; i += 32) s += p.partial[(size_t)(kd.cta0 + i) * D + c];
+  red[g][threadIdx.x & 31] = s;
   __syncthreads();
-  if (g == 0) {
+  s = red[threadIdx.x & 31][g];
 #pragma unroll
-    for (int i = 1; i < NG; ++i) s += red[i][c];
-    kd.dw[c] = s;
-  }
-}
-
-// Tokens per CTA and CTAs of each kind: about `target` rows a CTA; `most` > 0 bounds the CTAs
-// (persistent form), shared out by rows.
-int plan_kinds(NormParams& p, int target, int most) {
-  int64_t all = 0;
-  int grid = 0;
-  for (NormKind& k : p.kind)
-    if (k.ctas) all += k.heads;
-  for (NormKind& k : p.kind) {
-    k.cta0 = grid;
-    if (!k.ctas) continue;
-    k.tile = std::min(std::max(target / k.heads, 1), kNormMaxTile);
-    k.tiles = (p.T + k.tile - 1) / k.tile;
-    k.ctas = k.tiles;
-    if (most > 0) k.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(k.tiles, (int64_t)most * k.heads / all));
-    grid += k.ctas;
-  }
-  return grid;
-}
-
-// Rows per pass of one CTA, and passes per CTA: one while that leaves SMs idle, four (so that the
-// angles and the launch are shared by more rows) once there are enough rows.
-int target_rows(const NormParams& p, int D, int sms) {
-  int64_t heads = 0;
-  for (const NormKind& k : p.kind)
-    if (k.ctas) heads += k.heads;
-  const int pass = kThreads / (D / 16);
-  return heads * p.T > (int64_t)16 * sms * pass ? 4 * pass : pass;
+  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if ((threadIdx.x & 31) == 0) kd.dw[blockIdx.x % (D / 32) * 32 + g] = s;
 }
 
 template <typename T, int D>
 cudaError_t forward(NormParams p, int sms, cudaStream_t s) {
-  const int grid = plan_kinds(p, target_rows(p, D, sms), 0);
-  return launch_pdl(norm_rope_kernel<T, D>, dim3(grid), dim3(kThreads), 0, s, p);
+  constexpr int rpp = 512 / D, warps = kForwardThreads / 32;
+  // fewer passes a warp while that leaves warps of the machine idle
+  int64_t passes = 0;
+  for (NormKind& k : p.kind)
+    if (k.used) passes += (int64_t)p.T * ((k.heads + rpp - 1) / rpp);
+  const int64_t most = std::min<int64_t>(kUnitPasses, std::max<int64_t>(1, passes / ((int64_t)sms * kForwardCtas * warps)));
+  int grid = 0;
+  for (NormKind& k : p.kind) {
+    k.cta0 = grid;
+    k.ctas = 0;
+    if (!k.used) continue;
+    k.passes = (k.heads + rpp - 1) / rpp;
+    k.units = (int)((k.passes + most - 1) / most);
+    k.per_unit = (k.passes + k.units - 1) / k.units;
+    k.ctas = (int)(((int64_t)p.T * k.units + warps - 1) / warps);
+    grid += k.ctas;
+  }
+  return launch_pdl(norm_rope_kernel<T, D>, dim3(grid), dim3(kForwardThreads), 0, s, p);
 }
+
+std::atomic<uint64_t> g_limit[6];
 
 template <typename T, int D>
 cudaError_t backward(NormParams p, int sms, cudaStream_t s) {
-  const int grid = plan_kinds(p, target_rows(p, D, sms), std::min(3 * sms, kNormPartials - 2));
-  cudaError_t e = launch_pdl(norm_rope_backward_kernel<T, D>, dim3(grid), dim3(kThreads), 0, s, p);
+  constexpr int rpp = 512 / D, smem = kWarps * Ring<T, backward_stages<T>()>::kBytes;
+  constexpr int which = (D == 128 ? 3 : 0) + (sizeof(T) == 4 ? 2 : std::is_same<T, __half>::value ? 1 : 0);
+  cudaError_t e = ensure_smem_limit(norm_rope_backward_kernel<T, D>, smem, g_limit[which]);
+  if (e != cudaSuccess) return e;
+  // CTAs shared out by the kinds' passes, one pass a CTA at least
+  const int most = std::min(kBackwardCtas * sms, kNormPartials - 2);
+  int64_t all = 0;
+  for (NormKind& k : p.kind) {
+    k.passes = k.used ? (k.heads + rpp - 1) / rpp : 0;
+    all += k.passes;
+  }
+  int grid = 0;
+  for (NormKind& k : p.kind) {
+    k.cta0 = grid;
+    const int64_t share = std::max<int64_t>(1, (most * k.passes + all / 2) / all);
+    k.ctas = (int)std::min<int64_t>(share, (int64_t)p.T * k.passes);
+    grid += k.ctas;
+  }
+  e = launch_pdl(norm_rope_backward_kernel<T, D>, dim3(grid), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess || !(p.kind[0].dw || p.kind[1].dw)) return e;
-  return launch_pdl(norm_weight_kernel<D>, dim3(2), dim3(kReduceThreads), 0, s, p);
+  return launch_pdl(norm_weight_kernel<D>, dim3(2 * (D / 32)), dim3(1024), 0, s, p);
 }
 
 }  // namespace

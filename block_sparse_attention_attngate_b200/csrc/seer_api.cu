@@ -969,14 +969,14 @@ seer_status seer_page_release(int32_t batch, int32_t page_size, int32_t num_page
 
 namespace {
 
-constexpr int32_t kMaxNormTokens = 1 << 27;   // three kinds of one token a CTA stay inside the grid limit
 
 seer_status check_qk(const seer_qk_t* s) {
   if (!s) return fail(SEER_ERR_INVALID_ARG, "shape is NULL");
   if (s->num_tokens < 0 || s->num_q_heads < 1 || s->num_kv_heads < 1)
     return fail(SEER_ERR_INVALID_ARG, "num_tokens must be >= 0, num_q_heads and num_kv_heads >= 1");
-  if (s->num_tokens > kMaxNormTokens || s->num_q_heads > 65536 || s->num_kv_heads > 65536)
-    return fail(SEER_ERR_UNSUPPORTED, "num_tokens above 2^27 or more than 65536 heads");
+  if (s->num_q_heads > 65536 || s->num_kv_heads > 65536) return fail(SEER_ERR_UNSUPPORTED, "more than 65536 heads");
+  if ((int64_t)s->num_tokens * (s->num_q_heads + 2 * s->num_kv_heads) >= (int64_t)1 << 31)
+    return fail(SEER_ERR_UNSUPPORTED, "num_tokens * (num_q_heads + 2 * num_kv_heads) must be below 2^31");
   if (s->head_dim != 64 && s->head_dim != 128)
     return fail(SEER_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", s->head_dim);
   if (s->rope_dim < 0 || s->rope_dim > s->head_dim || s->rope_dim % 16)
@@ -1036,23 +1036,25 @@ seer_status check_pool(const seer_qk_t* s, const seer_pool_t* c, const char* nam
   return SEER_OK;
 }
 
-// Frequencies of (base, rope_dim); the thread's last set is kept, since 64 powers cost more than the launch.
-void rope_frequencies(float base, int rope_dim, double* theta) {
+// Frequencies of (base, rope_dim) in turns per position; the thread's last set is kept, since 64 powers cost
+// more than the launch.
+void rope_frequencies(float base, int rope_dim, double* turns) {
   static thread_local struct {
     float base = 0.f;
     int dim = 0;
-    double theta[seer::kMaxHalfGate];
+    double turns[seer::kMaxHalfGate];
   } last;
+  constexpr double kTwoPi = 6.283185307179586;
   if (last.base != base || last.dim != rope_dim) {
-    for (int i = 0; i < rope_dim / 2; ++i) last.theta[i] = pow((double)base, -2.0 * i / rope_dim);
+    for (int i = 0; i < rope_dim / 2; ++i) last.turns[i] = pow((double)base, -2.0 * i / rope_dim) / kTwoPi;
     last.base = base;
     last.dim = rope_dim;
   }
-  memcpy(theta, last.theta, rope_dim / 2 * sizeof(double));
+  memcpy(turns, last.turns, rope_dim / 2 * sizeof(double));
 }
 
 void norm_common(const seer_qk_t* s, seer::NormParams* p) {
-  rope_frequencies(s->rope_base, s->rope_dim, p->theta);
+  rope_frequencies(s->rope_base, s->rope_dim, p->turns);
   p->T = s->num_tokens;
   p->rope_dim = s->rope_dim;
   p->eps = s->eps;
@@ -1083,13 +1085,13 @@ seer_status seer_qk_norm_rope(const seer_qk_t* shape, const seer_rows_t* q, cons
   if ((st = check_written(shape, k_nope, H, "k_nope", &p.kind[1].nope)) != SEER_OK) return st;
   if ((st = check_pool(shape, k_cache, "k_cache", &p.kind[1].cache)) != SEER_OK) return st;
   if ((st = check_pool(shape, v_cache, "v_cache", &p.kind[2].cache)) != SEER_OK) return st;
-  p.kind[0].ctas = has(q_out) || has(q_nope);
-  p.kind[1].ctas = has(k_out) || has(k_nope) || p.kind[1].cache.data;
-  p.kind[2].ctas = p.kind[2].cache.data != nullptr;
-  if (!p.kind[0].ctas && !p.kind[1].ctas && !p.kind[2].ctas) return fail(SEER_ERR_INVALID_ARG, "no output");
+  p.kind[0].used = has(q_out) || has(q_nope);
+  p.kind[1].used = has(k_out) || has(k_nope) || p.kind[1].cache.data;
+  p.kind[2].used = p.kind[2].cache.data != nullptr;
+  if (!p.kind[0].used && !p.kind[1].used && !p.kind[2].used) return fail(SEER_ERR_INVALID_ARG, "no output");
   const char* const names[3] = {"q", "k", "v"};
   for (int i = 0; i < 3; ++i)
-    if (p.kind[i].ctas && !p.kind[i].x.data) return fail(SEER_ERR_INVALID_ARG, "%s is NULL but an output of it is not", names[i]);
+    if (p.kind[i].used && !p.kind[i].x.data) return fail(SEER_ERR_INVALID_ARG, "%s is NULL but an output of it is not", names[i]);
   const void* const outs[] = {p.kind[0].out.data, p.kind[1].out.data, p.kind[0].nope.data, p.kind[1].nope.data,
                               p.kind[1].cache.data, p.kind[2].cache.data};
   for (int i = 0; i < 6; ++i)
@@ -1159,8 +1161,8 @@ seer_status seer_qk_norm_rope_backward(const seer_qk_t* shape, const seer_rows_t
     if ((st = check_rows(shape, s.y, s.names[1], &kd.nope)) != SEER_OK) return st;
     if ((st = check_rows(shape, s.x, s.names[2], &kd.x)) != SEER_OK) return st;
     if ((st = check_written(shape, s.dx, kd.heads, s.names[3], &kd.dx)) != SEER_OK) return st;
-    kd.ctas = kd.dx.data != nullptr;
-    if (!kd.ctas) {
+    kd.used = kd.dx.data != nullptr;
+    if (!kd.used) {
       if (s.w || s.dw) return fail(SEER_ERR_INVALID_ARG, "%s is NULL but its norm weight or gradient is not", s.names[3]);
       continue;
     }
@@ -1174,7 +1176,7 @@ seer_status seer_qk_norm_rope_backward(const seer_qk_t* shape, const seer_rows_t
     kd.dw = s.dw;
     if (shape->rope_dim > 0 && kd.out.data && !positions) return fail(SEER_ERR_INVALID_ARG, "positions is NULL");
   }
-  if (!p.kind[0].ctas && !p.kind[1].ctas) return fail(SEER_ERR_INVALID_ARG, "no output");
+  if (!p.kind[0].used && !p.kind[1].used) return fail(SEER_ERR_INVALID_ARG, "no output");
   if (p.kind[0].dx.data == p.kind[1].dx.data || (dq_weight && dq_weight == dk_weight))
     return fail(SEER_ERR_INVALID_ARG, "two outputs share their memory");
   if (dq_weight || dk_weight) {

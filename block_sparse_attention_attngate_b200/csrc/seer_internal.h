@@ -271,13 +271,12 @@ struct NormKind {
   const void* weight; // [D] or null (no norm)
   float* dw;          // backward: [D] or null
   int32_t heads;
-  int32_t tile;       // tokens per CTA pass, at most kNormMaxTile
-  int32_t tiles;      // ceil(T / tile)
-  int32_t cta0;       // first CTA of the kind's range
-  int32_t ctas;       // and how many (0: the kind has nothing to do)
+  int32_t used;       // whether the kind has anything to do
+  // set by the launch: passes of a token's heads, units of a token and passes of a unit (forward), the kind's CTAs
+  int32_t passes, units, per_unit, cta0, ctas;
 };
 struct NormParams {
-  double theta[kMaxHalfGate];   // base^(-2i / rope_dim), i < rope_dim / 2
+  double turns[kMaxHalfGate];   // base^(-2i / rope_dim) / 2 pi, i < rope_dim / 2
   NormKind kind[3];             // query, key, value (values: cache copy only)
   const int32_t* positions;
   const int32_t* slot_map;
@@ -288,7 +287,6 @@ struct NormParams {
   float* partial;               // backward workspace [kNormPartials][D]
   int32_t* err;
 };
-constexpr int kNormMaxTile = 16;
 constexpr int kNormPartials = 1024;   // CTAs of the backward pass, at most
 cudaError_t launch_norm_rope(const NormParams& p, int D, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_norm_rope_backward(const NormParams& p, int D, int dtype, int sms, cudaStream_t s);

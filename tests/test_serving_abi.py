@@ -124,7 +124,7 @@ def forward(shape=None, **kw):
 
 
 def test_norm_rope_refusals():
-    for kw, st, word in ((dict(num_tokens=-1), 1, "num_tokens"), (dict(num_tokens=(1 << 27) + 1), 2, "2^27"),
+    for kw, st, word in ((dict(num_tokens=-1), 1, "num_tokens"), (dict(num_tokens=1 << 28), 2, "2^31"),
                          (dict(num_q_heads=0), 1, "heads"), (dict(head_dim=96), 2, "head_dim"),
                          (dict(rope_dim=24), 2, "rope_dim"), (dict(rope_dim=144), 2, "rope_dim"),
                          (dict(rope_dim=-16), 2, "rope_dim"), (dict(dtype=3), 2, "dtype"), (dict(rope_base=0), 1, "rope_base"),
