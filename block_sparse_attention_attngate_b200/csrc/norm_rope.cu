@@ -9,8 +9,11 @@
 // Backward, with r = 1 / sqrt(mean(x^2) + eps):
 //   dy = R^T dz + dy',   dx = r (w dy) - x r^3 mean(w dy x),   dw = sum dy x r
 //
-// Bound: HBM -- every input is read once and every output written once.  The arithmetic is close behind it, so it
-// is done two channels at a time (f32x2 instructions) and the addresses are stepped, not computed.
+// Bound: HBM -- every input is read once and every output written once.  Measured (graphs of the call, against the
+// copy bandwidth): 8192 tokens of 32 + 8 heads of 128, rotated and plain outputs and both caches in bf16, 51 us, 86 %
+// (the time does not move with the batch, the unit or the CTAs an SM); the gradients of the same rows 49 us, 79 %; 2049
+// tokens of 40 + 8 heads, half rotated, 11 us, 71 %.  The arithmetic is close behind the memory in the last two, so
+// it is done two channels at a time (f32x2 instructions: 53 us against 50 without) and addresses are stepped.
 //
 // Layout.  D / 16 lanes share a row, two 8-channel chunks (16 bytes in 16-bit types) each:
 // lane l of a row takes chunks l and l + rope_dim / 16 while those are
@@ -23,10 +26,9 @@
 // A pass is 32 / (D / 16) heads of one token.  Warps are independent.  A token's angles (fp64 products, whole
 // turns taken off) are computed by the warp's lanes while the token's first rows are on their way, exchanged
 // through the warp's own shared memory and kept in registers for all its heads.
-// Forward, a warp takes up to kUnitPasses passes of one token and ends; its rows, position, slot and the live count are
-// all requested at once.  Backward, warps stay (the weight gradients are sums over tokens): each takes an equal run
-// of the list of all passes and keeps passes in flight through a ring in shared memory (cp.async; every lane
-// reads back what it has requested itself, so no lane waits for another).
+// A warp takes up to kUnitPasses passes and ends; a unit's first rows, position, slot and the live count are
+// all requested at once.  (Staying CTAs with equal shares measured 10-20 % slower in both directions: some SMs
+// get less of the memory's bandwidth than others, and the rest wait for them at the end.)
 #include "seer_device.cuh"
 #include "seer_internal.h"
 
@@ -38,9 +40,9 @@
 namespace seer {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kBackwardCtas = 2;   // per SM
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kForwardCtas = 5, kBackwardCtas = 4;   // per SM, at least
+constexpr int kUnitPasses = 8, kRunPasses = 8;       // of a warp, forward and backward
 
 // ---------------------------------------------------------------- two channels at a time
 struct F2 {
@@ -175,7 +177,9 @@ __device__ __forceinline__ void token_angles(const NormParams& p, int pos, int c
                                              F2 (&s)[4]) {
   const int half = p.rope_dim >> 1;
   for (int i = threadIdx.x & 31; i < half; i += 32) {
-    const double turns = (double)pos * p.turns[i];
+    double turns;   // by its generic address: an indexed constant load would serve the lanes one after another
+    asm("ld.f64 %0, [%1];" : "=d"(turns) : "l"(&p.turns[i]));
+    turns *= pos;
     float x, y;
     sincospif((float)(2.0 * (turns - rint(turns))), &y, &x);   // the whole turns go in 64 bits, exactly
     cs[i] = x;
@@ -201,33 +205,24 @@ __device__ __forceinline__ T* lane_row(const Rows& r, int t, int h, int c0) {
   return static_cast<T*>(r.data) + (int64_t)t * r.stride_t + (int64_t)h * r.stride_h + c0;
 }
 
-// This CTA's kind, and this warp's run of its passes: [first, first + count).
+// This CTA's kind.
 __device__ __forceinline__ int cta_kind(const NormParams& p) {
   int k = 0;
   while (k < 2 && blockIdx.x >= p.kind[k].cta0 + p.kind[k].ctas) ++k;
   return k;
 }
-__device__ __forceinline__ void warp_run(const NormKind& kd, int live, int batch, int64_t* first, int* count) {
-  const int total = live * kd.passes, W = kd.ctas * kWarps;
-  int run = (total + W - 1) / W;
-  if (run > 2 * batch) run = (run + batch - 1) / batch * batch;
-  *first = (int64_t)((threadIdx.x >> 5) * kd.ctas + (blockIdx.x - kd.cta0)) * run;
-  *count = (int)min((int64_t)run, total - *first);
-}
 
-constexpr int kForwardThreads = 128, kForwardCtas = 5;
-constexpr int kBatch = 4;        // passes requested at once
-constexpr int kUnitPasses = 8;   // of a warp, at most
+constexpr int kForwardBatch = 3;   // passes requested at once, in 16-bit types (4 spill: 11.9 us against 10.9 at odd sizes)
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kForwardThreads, kForwardCtas) norm_rope_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, kForwardCtas) norm_rope_kernel(const __grid_constant__ NormParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;   // lanes per row, rows per pass
-  constexpr int B = sizeof(T) == 4 ? kBatch / 2 : kBatch;
-  __shared__ __align__(16) float angles[kForwardThreads / 32][2 * kMaxHalfGate];
+  constexpr int B = sizeof(T) == 4 ? 2 : kForwardBatch;
+  __shared__ __align__(16) float angles[kWarps][2 * kMaxHalfGate];
   const int which = cta_kind(p);
   const NormKind& kd = p.kind[which];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane & (LPR - 1);
-  const int unit = (blockIdx.x - kd.cta0) * (kForwardThreads / 32) + warp;
+  const int unit = (blockIdx.x - kd.cta0) * (kWarps) + warp;
   const int t = unit / kd.units, j = (unit - t * kd.units) * kd.per_unit;
   if (t >= p.T) return;
   int c0, c1;
@@ -346,12 +341,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return r;
 }
 
-// A ring of STAGES passes of three arrays' chunks (x, gradient of the rotated rows, of the un-rotated ones), a
+// A ring of STAGES passes of N arrays' chunks (x, gradient of the rotated rows, of the un-rotated ones), a
 // lane's 16 bytes beside its neighbours'.
-template <typename T, int STAGES>
+template <typename T, int N, int STAGES>
 struct Ring {
   static constexpr int kHalf = (int)sizeof(Chunk<T>) / 16;   // pieces of a chunk
-  static constexpr int kStage = 3 * 2 * kHalf * 512, kBytes = STAGES * kStage;   // per warp
+  static constexpr int kStage = N * 2 * kHalf * 512, kBytes = STAGES * kStage;   // per warp
   static __device__ __forceinline__ void request(uint32_t at, int array, const char* lo, int gap) {
 #pragma unroll
     for (int i = 0; i < 2 * kHalf; ++i)
@@ -368,16 +363,16 @@ struct Ring {
 template <typename T>
 constexpr int backward_stages() { return sizeof(T) == 4 ? 2 : 4; }
 
-// Backward: the weight gradient of a lane's 16 channels stays in registers; at the end the lanes, then the CTA's warps
-// are added up in a fixed order and go to the CTA's row of the workspace.
-template <typename T, int D>
+// Backward: the weight gradient of a lane's 16 channels stays in registers over the warp's passes; at the end the lanes
+// and warps of the CTA are added up in a fixed order and go to the CTA's row of the workspace.
+// Y: whether the un-rotated rows have a gradient.
+template <typename T, int D, bool Y>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_kernel(const __grid_constant__ NormParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
   constexpr int STAGES = backward_stages<T>();
-  using R = Ring<T, STAGES>;
+  using R = Ring<T, Y ? 3 : 2, STAGES>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float angles[kWarps][2 * kMaxHalfGate];
-  __shared__ float sums[kWarps][D];
   const int which = cta_kind(p);
   const NormKind& kd = p.kind[which];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, l = lane & (LPR - 1);
@@ -388,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
   pdl_wait();
   pdl_trigger();
   const int live = live_rows(p);
-  int64_t first;
-  int left;
-  warp_run(kd, live, 1, &first, &left);
+  const int total = live * kd.passes;
+  const int64_t first = ((int64_t)(blockIdx.x - kd.cta0) * kWarps + warp) * kd.run;   // of the list of all passes
+  int left = (int)min((int64_t)kd.run, total - first);
   F2 dw0[4] = {}, dw1[4] = {};
   if (left > 0) {
     int t = (int)first / kd.passes, j = (int)first - t * kd.passes;
@@ -409,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
         if (rj * RPP + sub < kd.heads) {   // rows that are not there stay unread
           if (kd.weight) R::request(at, 0, sx, gap);
           if (kd.out.data) R::request(at, 1, sz, gap);
-          if (kd.nope.data) R::request(at, 2, sy, gap);
+          if (Y && kd.nope.data) R::request(at, 2, sy, gap);
         }
         --ahead;
         if (++rj == kd.passes) {
@@ -419,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
         } else {
           sx += RPP * (int)sizeof(T) * kd.x.stride_h;
           sz += RPP * (int)sizeof(T) * kd.out.stride_h;
-          sy += RPP * (int)sizeof(T) * kd.nope.stride_h;
+          if (Y) sy += RPP * (int)sizeof(T) * kd.nope.stride_h;
         }
       }
       cp_commit();
@@ -445,12 +440,11 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
       for (int i = 0; i < n; ++i) {
         cp_wait<STAGES - 2>();
         const bool mine = room > 0;
-        Chunk<T> x0 = {}, x1 = {}, z0 = {}, z1 = {}, y0 = {}, y1 = {};
-        if (mine) {
-          if (kd.weight) R::read(at, 0, &x0, &x1);
-          if (kd.out.data) R::read(at, 1, &z0, &z1);
-          if (kd.nope.data) R::read(at, 2, &y0, &y1);
-        }
+        // a row that is not there reads whatever lies in the ring: it meets no other row and is not stored
+        Chunk<T> x0, x1, z0 = {}, z1 = {}, y0, y1;
+        R::read(at, 0, &x0, &x1);
+        if (kd.out.data) R::read(at, 1, &z0, &z1);
+        if (Y && kd.nope.data) R::read(at, 2, &y0, &y1);
         request(prev);
         prev = at;
         at = at == ring + (STAGES - 1) * R::kStage ? ring : at + R::kStage;
@@ -458,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
         unpack(z0, a);
         unpack(z1, b);
         if (rot && turn) rotate<true>(a, b, c, s);
-        if (kd.nope.data) {
+        if (Y && kd.nope.data) {
           F2 ya[4], yb[4];
           unpack(y0, ya);
           unpack(y1, yb);
@@ -494,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
           const F2 r2 = f2(rs, rs), k2 = f2(k, k);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (mine) {   // an eps of zero makes a row of zeros infinite
+            if (mine) {
               dw0[e] = fma2(a[e], mul2(xa[e], r2), dw0[e]);
               dw1[e] = fma2(b[e], mul2(xb[e], r2), dw1[e]);
             }
@@ -515,58 +509,60 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
     }
   }
   if (!kd.weight) return;
+  cp_wait<0>();
+  __syncwarp();   // the ring's memory is free
+  static_assert(R::kBytes >= RPP * D * 4, "a warp's sums fit its ring");
+  auto sums = [&](int w) { return reinterpret_cast<float*>(smem + w / RPP * R::kBytes) + w % RPP * D; };
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float2 x = split(dw0[e]), y = split(dw1[e]);
-#pragma unroll
-    for (int off = LPR; off < 32; off <<= 1) {
-      x.x += __shfl_xor_sync(0xffffffffu, x.x, off);
-      x.y += __shfl_xor_sync(0xffffffffu, x.y, off);
-      y.x += __shfl_xor_sync(0xffffffffu, y.x, off);
-      y.y += __shfl_xor_sync(0xffffffffu, y.y, off);
-    }
-    if (sub == 0) {
-      *reinterpret_cast<float2*>(&sums[warp][c0 + 2 * e]) = x;
-      *reinterpret_cast<float2*>(&sums[warp][c1 + 2 * e]) = y;
-    }
+  for (int e = 0; e < 4; e += 2) {
+    const float2 x = split(dw0[e]), x2 = split(dw0[e + 1]), y = split(dw1[e]), y2 = split(dw1[e + 1]);
+    *reinterpret_cast<float4*>(sums(warp * RPP + sub) + c0 + 2 * e) = make_float4(x.x, x.y, x2.x, x2.y);
+    *reinterpret_cast<float4*>(sums(warp * RPP + sub) + c1 + 2 * e) = make_float4(y.x, y.y, y2.x, y2.y);
   }
   __syncthreads();
   if (threadIdx.x < D) {
     float x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) x += sums[w][threadIdx.x];
+    for (int w = 0; w < kWarps * RPP; ++w) x += sums(w)[threadIdx.x];
     p.partial[(size_t)blockIdx.x * D + threadIdx.x] = x;
   }
 }
 
-// Sums of the CTAs' partial weight gradients in a fixed order: 32 channels of one kind a CTA, 32 threads each.
+// Sums of the CTAs' partial weight gradients in a fixed order: eight channels of one kind a CTA, 128 threads each.
 template <int D>
 __global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float red[32][33];
-  const int k = blockIdx.x / (D / 32), c = blockIdx.x % (D / 32) * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+  __shared__ float red[32][8];
+  const int k = blockIdx.x / (D / 8), c = blockIdx.x % (D / 8) * 8 + (threadIdx.x & 7), g = threadIdx.x >> 3;
+  const NormKind& kd = p.kind[k];
   pdl_wait();
   pdl_trigger();
-  const NormKind& kd = p.kind[k];
   if (!kd.dw) return;
   float s = 0.f;
 #pragma unroll 8
-  for (int i = g; i < kd.ctas; i += 32) s += p.partial[(size_t)(kd.cta0 + i) * D + c];
-  red[g][threadIdx.x & 31] = s;
+  for (int i = g; i < kd.ctas; i += 128) s += p.partial[(size_t)(kd.cta0 + i) * D + c];
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][threadIdx.x & 7] = s;
   __syncthreads();
-  s = red[threadIdx.x & 31][g];
+  if (threadIdx.x < 8) {
 #pragma unroll
-  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if ((threadIdx.x & 31) == 0) kd.dw[blockIdx.x % (D / 32) * 32 + g] = s;
+    for (int w = 1; w < 32; ++w) s += red[w][threadIdx.x];
+    kd.dw[c] = s;
+  }
+}
+
+// Passes a warp takes: `most`, fewer while that leaves warps of the machine idle.
+int64_t warp_passes(const NormParams& p, int rpp, int64_t warps, int64_t most) {
+  int64_t passes = 0;
+  for (const NormKind& k : p.kind)
+    if (k.used) passes += (int64_t)p.T * ((k.heads + rpp - 1) / rpp);
+  return std::min(most, std::max<int64_t>(1, passes / warps));
 }
 
 template <typename T, int D>
 cudaError_t forward(NormParams p, int sms, cudaStream_t s) {
-  constexpr int rpp = 512 / D, warps = kForwardThreads / 32;
-  // fewer passes a warp while that leaves warps of the machine idle
-  int64_t passes = 0;
-  for (NormKind& k : p.kind)
-    if (k.used) passes += (int64_t)p.T * ((k.heads + rpp - 1) / rpp);
-  const int64_t most = std::min<int64_t>(kUnitPasses, std::max<int64_t>(1, passes / ((int64_t)sms * kForwardCtas * warps)));
+  constexpr int rpp = 512 / D;
+  const int64_t most = warp_passes(p, rpp, (int64_t)sms * kForwardCtas * kWarps, kUnitPasses);
   int grid = 0;
   for (NormKind& k : p.kind) {
     k.cta0 = grid;
@@ -575,37 +571,41 @@ cudaError_t forward(NormParams p, int sms, cudaStream_t s) {
     k.passes = (k.heads + rpp - 1) / rpp;
     k.units = (int)((k.passes + most - 1) / most);
     k.per_unit = (k.passes + k.units - 1) / k.units;
-    k.ctas = (int)(((int64_t)p.T * k.units + warps - 1) / warps);
+    k.ctas = (int)(((int64_t)p.T * k.units + kWarps - 1) / kWarps);
     grid += k.ctas;
   }
-  return launch_pdl(norm_rope_kernel<T, D>, dim3(grid), dim3(kForwardThreads), 0, s, p);
+  return launch_pdl(norm_rope_kernel<T, D>, dim3(grid), dim3(kThreads), 0, s, p);
 }
 
-std::atomic<uint64_t> g_limit[6];
+std::atomic<uint64_t> g_limit[12];
 
-template <typename T, int D>
-cudaError_t backward(NormParams p, int sms, cudaStream_t s) {
-  constexpr int rpp = 512 / D, smem = kWarps * Ring<T, backward_stages<T>()>::kBytes;
-  constexpr int which = (D == 128 ? 3 : 0) + (sizeof(T) == 4 ? 2 : std::is_same<T, __half>::value ? 1 : 0);
-  cudaError_t e = ensure_smem_limit(norm_rope_backward_kernel<T, D>, smem, g_limit[which]);
+template <typename T, int D, bool Y>
+cudaError_t backward_of(NormParams p, int sms, cudaStream_t s) {
+  constexpr int rpp = 512 / D, smem = kWarps * Ring<T, Y ? 3 : 2, backward_stages<T>()>::kBytes;
+  constexpr int which = (Y ? 6 : 0) + (D == 128 ? 3 : 0) + (sizeof(T) == 4 ? 2 : std::is_same<T, __half>::value ? 1 : 0);
+  cudaError_t e = ensure_smem_limit(norm_rope_backward_kernel<T, D, Y>, smem, g_limit[which]);
   if (e != cudaSuccess) return e;
-  // CTAs shared out by the kinds' passes, one pass a CTA at least
-  const int most = std::min(kBackwardCtas * sms, kNormPartials - 2);
-  int64_t all = 0;
-  for (NormKind& k : p.kind) {
-    k.passes = k.used ? (k.heads + rpp - 1) / rpp : 0;
-    all += k.passes;
-  }
+  const int64_t run = warp_passes(p, rpp, (int64_t)sms * kBackwardCtas * kWarps, kRunPasses);
+  constexpr int64_t rows = (int64_t)kNormPartials / 2 * kWarps;   // warps of a kind, at most
   int grid = 0;
   for (NormKind& k : p.kind) {
     k.cta0 = grid;
-    const int64_t share = std::max<int64_t>(1, (most * k.passes + all / 2) / all);
-    k.ctas = (int)std::min<int64_t>(share, (int64_t)p.T * k.passes);
+    k.ctas = 0;
+    if (!k.used) continue;
+    k.passes = (k.heads + rpp - 1) / rpp;
+    const int64_t all = (int64_t)p.T * k.passes;
+    k.run = (int)std::max(run, (all + rows - 1) / rows);
+    k.ctas = (int)((all + (int64_t)k.run * kWarps - 1) / ((int64_t)k.run * kWarps));
     grid += k.ctas;
   }
-  e = launch_pdl(norm_rope_backward_kernel<T, D>, dim3(grid), dim3(kThreads), smem, s, p);
+  e = launch_pdl(norm_rope_backward_kernel<T, D, Y>, dim3(grid), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess || !(p.kind[0].dw || p.kind[1].dw)) return e;
-  return launch_pdl(norm_weight_kernel<D>, dim3(2 * (D / 32)), dim3(1024), 0, s, p);
+  return launch_pdl(norm_weight_kernel<D>, dim3(2 * (D / 8)), dim3(1024), 0, s, p);
+}
+
+template <typename T, int D>
+cudaError_t backward(const NormParams& p, int sms, cudaStream_t s) {
+  return p.kind[0].nope.data || p.kind[1].nope.data ? backward_of<T, D, true>(p, sms, s) : backward_of<T, D, false>(p, sms, s);
 }
 
 }  // namespace

@@ -272,8 +272,8 @@ struct NormKind {
   float* dw;          // backward: [D] or null
   int32_t heads;
   int32_t used;       // whether the kind has anything to do
-  // set by the launch: passes of a token's heads, units of a token and passes of a unit (forward), the kind's CTAs
-  int32_t passes, units, per_unit, cta0, ctas;
+  // set by the launch: passes of a token's heads, units of a token, passes of a unit, passes of a warp (backward), the kind's CTAs
+  int32_t passes, units, per_unit, run, cta0, ctas;
 };
 struct NormParams {
   double turns[kMaxHalfGate];   // base^(-2i / rope_dim) / 2 pi, i < rope_dim / 2
@@ -287,7 +287,7 @@ struct NormParams {
   float* partial;               // backward workspace [kNormPartials][D]
   int32_t* err;
 };
-constexpr int kNormPartials = 1024;   // CTAs of the backward pass, at most
+constexpr int kNormPartials = 8192;   // CTAs of the backward pass, at most
 cudaError_t launch_norm_rope(const NormParams& p, int D, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_norm_rope_backward(const NormParams& p, int D, int dtype, int sms, cudaStream_t s);
 

@@ -528,7 +528,7 @@ typedef struct {
  *         (rotate-half pairing, angles reduced in fp64)
  *   q_out / k_out = z, q_nope / k_nope = y, k_cache[slot_map[t]] = z (keys), v_cache[slot_map[t]] = v[t]
  * each rounded once from fp32.  Absent outputs are not written; rows at or behind *live_tokens are
- * neither read nor written.  A slot of -1 is not written; any other slot outside the pool sets
+ * not used and nothing is written for them.  A slot of -1 is not written; any other slot outside the pool sets
  * SEER_DEVERR_PAGE_INDEX and is not written.  Slots of live rows must be distinct (else which
  * row's channels remain is undefined).
  *

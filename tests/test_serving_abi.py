@@ -157,7 +157,7 @@ def test_norm_rope_refusals():
 
 def backward(shape=None, **kw):
     a = dict(gq=rows(), gk=rows(1 << 16), gqn=None, gkn=None, q=rows(1 << 17), k=rows(1 << 18), wq=P, wk=P, pos=P,
-             dq=rows(1 << 19), dk=rows(1 << 20), dwq=P, dwk=ctypes.c_void_p(8192), live=None, ws=P, n=1 << 20)
+             dq=rows(1 << 19), dk=rows(1 << 20), dwq=P, dwk=ctypes.c_void_p(8192), live=None, ws=P, n=1 << 23)
     a.update(kw)
     s = shape or qk()
     args = [ctypes.byref(x) if isinstance(x, ctypes.Structure) else x for x in a.values()]
@@ -166,7 +166,7 @@ def backward(shape=None, **kw):
 
 def test_norm_rope_backward_refusals():
     n = lib.seer_qk_norm_rope_workspace_bytes(128)
-    assert n == 1024 * 128 * 4 and lib.seer_qk_norm_rope_workspace_bytes(96) == 0
+    assert n == 8192 * 128 * 4 and lib.seer_qk_norm_rope_workspace_bytes(96) == 0
     assert backward(qk(head_dim=80)) == 2
     assert backward(dq=None, dk=None, wq=None, wk=None, dwq=None, dwk=None) == 1 and said("no output")
     assert backward(dq=None) == 1 and said("norm weight")
