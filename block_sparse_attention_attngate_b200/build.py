@@ -1,12 +1,13 @@
-"""Build libseer.so (sm_100a) in-tree with nvcc.
+"""Build libseer.so (sm_100a) in-tree with nvcc, and the Python call layer _seer_call.so beside it.
 
     python -m block_sparse_attention_attngate_b200.build [--force] [--verbose]
 
 Each csrc/*.cu compiles to an object under _build/, then everything links
 into block_sparse_attention_attngate_b200/libseer.so with the CUDA runtime
 linked statically (the library does not depend on which libcudart a host
-process loaded).  A rebuild happens only when a source or header is newer
-than the library.
+process loaded).  csrc/binding.cpp, which checks tensors for the binding,
+compiles against torch's headers with g++.  A rebuild happens only when a
+source or header is newer than what is built from it.
 """
 
 from __future__ import annotations
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +26,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libseer.so")
+CALL_SRC = os.path.join(CSRC, "binding.cpp")
+CALL = os.path.join(PKG, "_seer_call.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2",
@@ -53,7 +57,30 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def build_call_layer(force: bool = False, verbose: bool = False) -> str:
+    deps = [CALL_SRC, os.path.join(INCLUDE, "seer.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(CALL) and all(os.path.getmtime(f) <= os.path.getmtime(CALL) for f in deps):
+        return CALL
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [os.path.join(os.path.dirname(torch.__file__), "include"), sysconfig.get_paths()["include"], cuda]
+    tmp = CALL + ".tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for i in includes for x in ("-isystem", i)], "-I", INCLUDE, CALL_SRC, "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
+    return CALL
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_call_layer(force, verbose)
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

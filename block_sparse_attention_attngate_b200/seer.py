@@ -9,10 +9,9 @@ this module raises at import time -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
-import struct
-import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -111,7 +110,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "seer_prefill_gt": (I32, [DP, P, I32, KP, KP, P, P, P, P, P, SZ, P, P]),
         "seer_page_plan": (I32, [I32] * 5 + [P] * 12),
         "seer_page_release": (I32, [I32] * 4 + [P] * 9),
-        # descriptors of these by address (see _Scratch)
+        # descriptors of these by address
         "seer_qk_norm_rope": (I32, [P] * 17),
         "seer_qk_norm_rope_workspace_bytes": (SZ, [I32]),
         "seer_qk_norm_rope_backward": (I32, [P] * 16 + [SZ, P]),
@@ -131,6 +130,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 _lib = load_library()
+
+
+def _load_call_layer():
+    """The compiled call layer of the operators around the decode step, bound to the loaded library."""
+    path = os.path.join(_HERE, "_seer_call.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m block_sparse_attention_attngate_b200.build`")
+    spec = importlib.util.spec_from_file_location("_seer_call", path)
+    layer = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(layer)
+    for name in layer.entries():
+        layer.bind(name, ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value)
+    return layer
+
+
+_call = _load_call_layer()
 
 
 def version() -> str:
@@ -635,48 +650,9 @@ def gate_truth(shape: Shape, q: torch.Tensor, k: KVCache, seqlens: torch.Tensor,
                                 _ptr(err), _stream(stream)))
 
 
-# The calls around the decode step take many small tensors and run for a few microseconds, so their checks come in two
-# forms: one short test that every argument is as it must be, and, where it fails, the named checks, which say what is wrong.
-
-def _fits(t, shape, dtype, dev) -> bool:
-    """A contiguous tensor of this shape (a tuple of ints), type and device."""
-    return t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-
-
-def _fits_or_none(t, shape, dtype, dev) -> bool:
-    return t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous())
-
-
-def _on_current(t) -> int:
-    """Index of t's device when it is the current one, else -2 (which no tensor has)."""
-    dev = t.get_device()
-    return dev if dev >= 0 and torch._C._cuda_getDevice() == dev else -2
-
-
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-class _Scratch(threading.local):
-    """Per-thread memory of the descriptors that a call hands to the library (read during the call only)."""
-
-    def __init__(self):
-        self.rows, self.pools, self.qk, self.dense = (RowsDesc * 8)(), (PoolDesc * 2)(), QkShape(), DenseShape()
-        size, at = ctypes.sizeof(RowsDesc), ctypes.addressof(self.rows)
-        self.rows_at = [at + i * size for i in range(8)]
-        size, at = ctypes.sizeof(PoolDesc), ctypes.addressof(self.pools)
-        self.pools_at = [at, at + size]
-        self.qk_at, self.dense_at = ctypes.addressof(self.qk), ctypes.addressof(self.dense)
-
-
-_scratch = _Scratch()
-_pack_row, _pack_pool = struct.Struct("Pqq"), struct.Struct("Pqqqqi")
-_pack_qk, _pack_dense = struct.Struct("iiiiiiff"), struct.Struct("iiiiiiif")
-
+# The calls around the decode step run for a few microseconds and take many small tensors, so a compiled call layer
+# (csrc/binding.cpp) makes them when every argument is as it must be.  Where one is not, it leaves the call to the checks
+# below, which say what is wrong.
 
 def page_plan(page_size: int, seqlens: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor,
               free_list: torch.Tensor, free_count: torch.Tensor, cu_tokens: torch.Tensor, slot_map: torch.Tensor,
@@ -687,31 +663,29 @@ def page_plan(page_size: int, seqlens: torch.Tensor, new_tokens: torch.Tensor, b
     block_table int32 [B, width] and free_list int32 [num_pages] are as the caller keeps them; lengths and the free
     count are updated in place unless seqlens_out / free_count_out are given.  cu_tokens int32 [B + 1]; slot_map and
     positions int32 [room], filled with -1 / 0 behind the last token."""
-    B, pages, dev = _page_args(page_size, seqlens, new_tokens, "new_tokens", block_table, free_list, free_count)
+    status = _call.page_plan(page_size, seqlens, new_tokens, block_table, free_list, free_count, cu_tokens, slot_map, positions,
+                             seqlens_out, free_count_out, err, stream)
+    if status >= 0:
+        return _check(status)
+    B = _page_args(page_size, seqlens, new_tokens, "new_tokens", block_table, free_list, free_count)
     seqlens_out = seqlens if seqlens_out is None else seqlens_out
     free_count_out = free_count if free_count_out is None else free_count_out
-    i32, room = torch.int32, getattr(slot_map, "shape", None)
-    if not (dev >= 0 and room is not None and len(room) == 1 and room[0] >= 1 and _fits(seqlens_out, (B,), i32, dev)
-            and _fits(free_count_out, (1,), i32, dev) and _fits(cu_tokens, (B + 1,), i32, dev)
-            and _fits(slot_map, room, i32, dev) and _fits(positions, room, i32, dev)
-            and (err is None or _fits(err, err.shape, i32, dev) and err.numel() >= 1)):
-        _need_shape(seqlens_out, (B,), "seqlens_out")
-        _need_shape(free_count_out, (1,), "free_count_out")
-        _need_shape(cu_tokens, (B + 1,), "cu_tokens")
-        if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1 or slot_map.numel() < 1:
-            raise ValueError("slot_map must be a 1-D tensor of at least one slot")
-        _need_shape(positions, slot_map.shape, "positions")
-        _need_err(err)
-        for t, name in ((seqlens, "seqlens"), (new_tokens, "new_tokens"), (block_table, "block_table"),
-                        (free_list, "free_list"), (free_count, "free_count"), (seqlens_out, "seqlens_out"),
-                        (free_count_out, "free_count_out"), (cu_tokens, "cu_tokens"), (slot_map, "slot_map"),
-                        (positions, "positions")):
-            _need(t, torch.int32, name)
-    _check(_lib.seer_page_plan(B, page_size, pages, block_table.shape[1], room[0], seqlens.data_ptr(),
-                               new_tokens.data_ptr(), block_table.data_ptr(), free_list.data_ptr(),
-                               free_count.data_ptr(), seqlens_out.data_ptr(), free_count_out.data_ptr(),
-                               cu_tokens.data_ptr(), slot_map.data_ptr(), positions.data_ptr(), _address(err),
-                               _raw_stream(stream, dev)))
+    _need_shape(seqlens_out, (B,), "seqlens_out")
+    _need_shape(free_count_out, (1,), "free_count_out")
+    _need_shape(cu_tokens, (B + 1,), "cu_tokens")
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1 or slot_map.numel() < 1:
+        raise ValueError("slot_map must be a 1-D tensor of at least one slot")
+    _need_shape(positions, slot_map.shape, "positions")
+    _need_err(err)
+    for t, name in ((seqlens, "seqlens"), (new_tokens, "new_tokens"), (block_table, "block_table"),
+                    (free_list, "free_list"), (free_count, "free_count"), (seqlens_out, "seqlens_out"),
+                    (free_count_out, "free_count_out"), (cu_tokens, "cu_tokens"), (slot_map, "slot_map"),
+                    (positions, "positions")):
+        _need(t, torch.int32, name)
+    _check(_lib.seer_page_plan(B, int(page_size), free_list.numel(), block_table.shape[1], slot_map.numel(),
+                               _ptr(seqlens), _ptr(new_tokens), _ptr(block_table), _ptr(free_list), _ptr(free_count),
+                               _ptr(seqlens_out), _ptr(free_count_out), _ptr(cu_tokens), _ptr(slot_map),
+                               _ptr(positions), _ptr(err), _stream(stream)))
 
 
 def page_release(page_size: int, seqlens: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor,
@@ -719,115 +693,103 @@ def page_release(page_size: int, seqlens: torch.Tensor, finished: torch.Tensor, 
                  free_count_out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
     """Give the pages of sequences with finished != 0 back to the free list and set their lengths to 0 (see
     seer_page_release); in place unless seqlens_out / free_count_out are given."""
-    B, pages, dev = _page_args(page_size, seqlens, finished, "finished", block_table, free_list, free_count)
+    status = _call.page_release(page_size, seqlens, finished, block_table, free_list, free_count, seqlens_out, free_count_out,
+                                err, stream)
+    if status >= 0:
+        return _check(status)
+    B = _page_args(page_size, seqlens, finished, "finished", block_table, free_list, free_count)
     seqlens_out = seqlens if seqlens_out is None else seqlens_out
     free_count_out = free_count if free_count_out is None else free_count_out
-    i32 = torch.int32
-    if not (dev >= 0 and _fits(seqlens_out, (B,), i32, dev) and _fits(free_count_out, (1,), i32, dev)
-            and (err is None or _fits(err, err.shape, i32, dev) and err.numel() >= 1)):
-        _need_shape(seqlens_out, (B,), "seqlens_out")
-        _need_shape(free_count_out, (1,), "free_count_out")
-        _need_err(err)
-        for t, name in ((seqlens, "seqlens"), (finished, "finished"), (block_table, "block_table"),
-                        (free_list, "free_list"), (free_count, "free_count"), (seqlens_out, "seqlens_out"),
-                        (free_count_out, "free_count_out")):
-            _need(t, torch.int32, name)
-    _check(_lib.seer_page_release(B, page_size, pages, block_table.shape[1], seqlens.data_ptr(), finished.data_ptr(),
-                                  block_table.data_ptr(), free_list.data_ptr(), free_count.data_ptr(),
-                                  seqlens_out.data_ptr(), free_count_out.data_ptr(), _address(err),
-                                  _raw_stream(stream, dev)))
+    _need_shape(seqlens_out, (B,), "seqlens_out")
+    _need_shape(free_count_out, (1,), "free_count_out")
+    _need_err(err)
+    for t, name in ((seqlens, "seqlens"), (finished, "finished"), (block_table, "block_table"),
+                    (free_list, "free_list"), (free_count, "free_count"), (seqlens_out, "seqlens_out"),
+                    (free_count_out, "free_count_out")):
+        _need(t, torch.int32, name)
+    _check(_lib.seer_page_release(B, int(page_size), free_list.numel(), block_table.shape[1], _ptr(seqlens),
+                                  _ptr(finished), _ptr(block_table), _ptr(free_list), _ptr(free_count),
+                                  _ptr(seqlens_out), _ptr(free_count_out), _ptr(err), _stream(stream)))
 
 
-def _page_args(page_size, seqlens, per_request, name: str, block_table, free_list, free_count):
-    """(B, num_pages, device); the device is -1 when a tensor does not fit in a way that the caller reports."""
+def _page_args(page_size, seqlens, per_request, name: str, block_table, free_list, free_count) -> int:
     if not isinstance(seqlens, torch.Tensor) or seqlens.dim() != 1:
         raise ValueError("seqlens must be a 1-D tensor")
-    B, i32 = seqlens.shape[0], torch.int32
+    B = int(seqlens.shape[0])
+    _need_shape(per_request, (B,), name)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, pages)")
     if not isinstance(free_list, torch.Tensor) or free_list.dim() != 1:
         raise ValueError("free_list must be a 1-D tensor of num_pages entries")
-    dev = _on_current(seqlens)
-    if (dev >= 0 and seqlens.dtype is i32 and seqlens.is_contiguous() and isinstance(per_request, torch.Tensor)
-            and _fits(per_request, (B,), i32, dev) and _fits(block_table, block_table.shape, i32, dev)
-            and _fits(free_list, free_list.shape, i32, dev) and isinstance(free_count, torch.Tensor)
-            and _fits(free_count, (1,), i32, dev)):
-        return B, free_list.shape[0], dev
-    _need_shape(per_request, (B,), name)
     _need_shape(free_count, (1,), "free_count")
-    return B, free_list.shape[0], -1
+    return B
 
 
-def _rows(at: int, t: Optional[torch.Tensor], T: int, heads: int, d: int, dtype: torch.dtype, dev: int, name: str):
-    """Address of a seer_rows_t (the thread's at-th) of a [T, heads, d] view with unit-stride d (None: absent)."""
+def _rows(t: Optional[torch.Tensor], T: int, heads: int, d: int, dtype: torch.dtype, name: str):
+    """seer_rows_t of a [T, heads, d] view with unit-stride d (None: absent)."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.shape == (T, heads, d) and t.dtype is dtype and t.get_device() == dev):
-        _need_shape(t, (T, heads, d), name)
-        _need(t, dtype, name, contiguous=False)
-    st, sh, sc = t.stride()
-    if sc != 1:
+    _need_shape(t, (T, heads, d), name)
+    _need(t, dtype, name, contiguous=False)
+    if t.stride(2) != 1:
         raise ValueError(f"{name} must have unit-stride channels")
     # an axis of one element may carry any stride; none of it is used
-    _pack_row.pack_into(_scratch.rows, 24 * at, t.data_ptr(), st if T > 1 else heads * d, sh if heads > 1 else d)
-    return _scratch.rows_at[at]
+    return RowsDesc(t.data_ptr(), t.stride(0) if T > 1 else heads * d, t.stride(1) if heads > 1 else d)
 
 
-def _pool(at: int, t: Optional[torch.Tensor], heads: int, d: int, dtype: torch.dtype, dev: int, name: str):
-    """Address of a seer_pool_t (the thread's at-th) of a [pages, heads, page, d] view with unit-stride d (None: absent)."""
+def _ref(desc):
+    return None if desc is None else ctypes.byref(desc)
+
+
+def _pool(t: Optional[torch.Tensor], heads: int, d: int, dtype: torch.dtype, name: str):
+    """seer_pool_t of a [pages, heads, page, d] view with unit-stride d (None: absent)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[1] != heads or t.shape[3] != d:
         got = tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name} must be a [pages, {heads}, page, {d}] view, got {got}")
-    if not (t.dtype is dtype and t.get_device() == dev):
-        _need(t, dtype, name, contiguous=False)
-    sp, sh, st, sc = t.stride()
-    if sc != 1:
+    _need(t, dtype, name, contiguous=False)
+    if t.stride(3) != 1:
         raise ValueError(f"{name} must have unit-stride channels")
-    pages, _, page, _ = t.shape
-    # as in _rows, a stride that is never taken may be anything in torch's eyes: the library wants them in order
-    sh = sh if heads > 1 else st * page
-    _pack_pool.pack_into(_scratch.pools, 48 * at, t.data_ptr(), sp if pages > 1 else max(sh * heads, st * page), sh,
-                         st if page > 1 else max(st, d), pages, page)
-    return _scratch.pools_at[at]
+    pages, page = t.shape[0], t.shape[2]
+    st = t.stride(2) if page > 1 else d
+    sh = t.stride(1) if heads > 1 else st * page
+    return PoolDesc(t.data_ptr(), t.stride(0) if pages > 1 else sh * heads, sh, st, pages, page)
 
 
-def _qk_args(q, k, rope_base: float, rope_dim: Optional[int], eps: float):
-    """(device, T, Hq, Hkv, d, dtype, rope_dim) of query rows and / or key rows; packs the thread's QkShape."""
+def _qk_shape(q, k, rope_base: float, rope_dim: Optional[int], eps: float):
+    """(QkShape, T, Hq, Hkv, d, dtype) of query rows and / or key rows."""
     for t, name in ((q, "q"), (k, "k")):
         if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 3):
             raise ValueError(f"{name} must be a [tokens, heads, d] tensor")
     one = q if q is not None else k
     if one is None:
         raise ValueError("q or k is needed")
-    dt = one.dtype
-    if dt not in DTYPES:
-        raise TypeError(f"q and k must be one of {list(DTYPES)}, got {dt}")
-    T, Hq, d = one.shape
-    Hkv = k.shape[1] if k is not None else Hq
+    if one.dtype not in DTYPES:
+        raise TypeError(f"q and k must be one of {list(DTYPES)}, got {one.dtype}")
+    T, d = int(one.shape[0]), int(one.shape[2])
+    Hq = int(q.shape[1]) if q is not None else int(k.shape[1])
+    Hkv = int(k.shape[1]) if k is not None else Hq
     rope = d if rope_dim is None else int(rope_dim)
-    _pack_qk.pack_into(_scratch.qk, 0, T, Hq, Hkv, d, rope, DTYPES[dt], rope_base, eps)
-    return _on_current(one), T, Hq, Hkv, d, dt, rope
+    return QkShape(T, Hq, Hkv, d, rope, DTYPES[one.dtype], float(rope_base), float(eps)), T, Hq, Hkv, d, one.dtype
 
 
-def _norm_vector(t, d: int, dtype: torch.dtype, dev: int, name: str):
-    if t is not None and not (isinstance(t, torch.Tensor) and _fits(t, (d,), dtype, dev)):
-        _need_shape(t, (d,), name)
-        _need(t, dtype, name)
-    return None if t is None else t.data_ptr()
+def _norm_vectors(weights, d: int, dtype: torch.dtype):
+    for t, name in weights:
+        if t is not None:
+            _need_shape(t, (d,), name)
+            _need(t, dtype, name)
 
 
-def _token_args(positions, num_tokens, T: int, dev: int, need_positions: bool):
-    i32 = torch.int32
+def _token_args(positions, num_tokens, T: int, need_positions: bool):
     if positions is None and need_positions:
         raise ValueError("positions is needed (rope_dim > 0)")
-    if positions is not None and not (isinstance(positions, torch.Tensor) and _fits(positions, (T,), i32, dev)):
+    if positions is not None:
         _need_shape(positions, (T,), "positions")
-        _need(positions, i32, "positions")
-    if num_tokens is not None and not (isinstance(num_tokens, torch.Tensor) and _fits(num_tokens, (1,), i32, dev)):
+        _need(positions, torch.int32, "positions")
+    if num_tokens is not None:
         _need_shape(num_tokens, (1,), "num_tokens")
-        _need(num_tokens, i32, "num_tokens")
+        _need(num_tokens, torch.int32, "num_tokens")
 
 
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -844,23 +806,27 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions
     q_out / k_out, un-rotated (normalised) ones to q_nope / k_nope, keys and values to the rows slot_map [T] of the
     pools k_cache / v_cache [pages, Hkv, page, d]; whichever is None is not written.  num_tokens (int32 [1], on the
     device) cuts the rows to the first so many.  rope_dim defaults to d."""
-    dev, T, Hq, Hkv, d, dt, rope = _qk_args(q, k, rope_base, rope_dim, eps)
-    rq, rk = _rows(0, q, T, Hq, d, dt, dev, "q"), _rows(1, k, T, Hkv, d, dt, dev, "k")
-    rv = _rows(2, v, T, Hkv, d, dt, dev, "v")
-    rqo, rko = _rows(3, q_out, T, Hq, d, dt, dev, "q_out"), _rows(4, k_out, T, Hkv, d, dt, dev, "k_out")
-    rqn, rkn = _rows(5, q_nope, T, Hq, d, dt, dev, "q_nope"), _rows(6, k_nope, T, Hkv, d, dt, dev, "k_nope")
-    pk, pv = _pool(0, k_cache, Hkv, d, dt, dev, "k_cache"), _pool(1, v_cache, Hkv, d, dt, dev, "v_cache")
-    wq, wk = _norm_vector(q_weight, d, dt, dev, "q_weight"), _norm_vector(k_weight, d, dt, dev, "k_weight")
-    _token_args(positions, num_tokens, T, dev, rope > 0)
+    status = _call.qk_norm_rope(q, k, positions, q_out, k_out, q_weight, k_weight, rope_base, rope_dim, eps, q_nope, k_nope, v,
+                                k_cache, v_cache, slot_map, num_tokens, err, stream)
+    if status >= 0:
+        return _check(status)
+    shape, T, Hq, Hkv, d, dt = _qk_shape(q, k, rope_base, rope_dim, eps)
+    rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
+        (q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (q_out, Hq, "q_out"), (k_out, Hkv, "k_out"),
+        (q_nope, Hq, "q_nope"), (k_nope, Hkv, "k_nope"))]
+    pools = [_pool(t, Hkv, d, dt, name) for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"))]
+    _norm_vectors(((q_weight, "q_weight"), (k_weight, "k_weight")), d, dt)
+    _token_args(positions, num_tokens, T, shape.rope_dim > 0)
     if slot_map is not None:
-        if not (isinstance(slot_map, torch.Tensor) and _fits(slot_map, (T,), torch.int32, dev)):
-            _need_shape(slot_map, (T,), "slot_map")
-            _need(slot_map, torch.int32, "slot_map")
-    elif pk is not None or pv is not None:
+        _need_shape(slot_map, (T,), "slot_map")
+        _need(slot_map, torch.int32, "slot_map")
+    elif k_cache is not None or v_cache is not None:
         raise ValueError("slot_map is needed with a cache")
     _need_err(err)
-    _check(_lib.seer_qk_norm_rope(_scratch.qk_at, rq, rk, rv, wq, wk, _address(positions), rqo, rko, rqn, rkn, pk, pv,
-                                  _address(slot_map), _address(num_tokens), _address(err), _raw_stream(stream, dev)))
+    _check(_lib.seer_qk_norm_rope(ctypes.byref(shape), _ref(rows[0]), _ref(rows[1]), _ref(rows[2]), _ptr(q_weight),
+                                  _ptr(k_weight), _ptr(positions), _ref(rows[3]), _ref(rows[4]), _ref(rows[5]),
+                                  _ref(rows[6]), _ref(pools[0]), _ref(pools[1]), _ptr(slot_map), _ptr(num_tokens),
+                                  _ptr(err), _stream(stream)))
 
 
 def norm_workspace_bytes(head_dim: int) -> int:
@@ -883,26 +849,28 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     """Gradients of qk_norm_rope (see seer_qk_norm_rope_backward): dq / dk of the inputs q / k and fp32 [d] dq_weight /
     dk_weight, from the gradients of the rotated rows (dq_out, dk_out) and of the un-rotated ones (dq_nope, dk_nope);
     None: that output had none.  workspace: alloc_norm_workspace(d), needed with norm weights."""
-    dev, T, Hq, Hkv, d, dt, rope = _qk_args(q if q is not None else dq, k if k is not None else dk, rope_base, rope_dim,
-                                            eps)
-    rz, rkz = _rows(0, dq_out, T, Hq, d, dt, dev, "dq_out"), _rows(1, dk_out, T, Hkv, d, dt, dev, "dk_out")
-    ry, rky = _rows(2, dq_nope, T, Hq, d, dt, dev, "dq_nope"), _rows(3, dk_nope, T, Hkv, d, dt, dev, "dk_nope")
-    rq, rk = _rows(4, q, T, Hq, d, dt, dev, "q"), _rows(5, k, T, Hkv, d, dt, dev, "k")
-    rdq, rdk = _rows(6, dq, T, Hq, d, dt, dev, "dq"), _rows(7, dk, T, Hkv, d, dt, dev, "dk")
-    f32 = torch.float32
-    wq, wk = _norm_vector(q_weight, d, dt, dev, "q_weight"), _norm_vector(k_weight, d, dt, dev, "k_weight")
-    gq, gk = _norm_vector(dq_weight, d, f32, dev, "dq_weight"), _norm_vector(dk_weight, d, f32, dev, "dk_weight")
-    _token_args(positions, num_tokens, T, dev, rope > 0 and (rz is not None or rkz is not None))
+    status = _call.qk_norm_rope_backward(dq_out, dk_out, q, k, positions, dq, dk, workspace, q_weight, k_weight, dq_weight,
+                                         dk_weight, rope_base, rope_dim, eps, dq_nope, dk_nope, num_tokens, stream)
+    if status >= 0:
+        return _check(status)
+    shape, T, Hq, Hkv, d, dt = _qk_shape(q if q is not None else dq, k if k is not None else dk, rope_base, rope_dim, eps)
+    rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
+        (dq_out, Hq, "dq_out"), (dk_out, Hkv, "dk_out"), (dq_nope, Hq, "dq_nope"), (dk_nope, Hkv, "dk_nope"),
+        (q, Hq, "q"), (k, Hkv, "k"), (dq, Hq, "dq"), (dk, Hkv, "dk"))]
+    _norm_vectors(((q_weight, "q_weight"), (k_weight, "k_weight")), d, dt)
+    _norm_vectors(((dq_weight, "dq_weight"), (dk_weight, "dk_weight")), d, torch.float32)
+    _token_args(positions, num_tokens, T, shape.rope_dim > 0 and (dq_out is not None or dk_out is not None))
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    _check(_lib.seer_qk_norm_rope_backward(_scratch.qk_at, rz, rkz, ry, rky, rq, rk, wq, wk, _address(positions), rdq, rdk,
-                                           gq, gk, _address(num_tokens), _address(workspace),
-                                           0 if workspace is None else workspace.numel(), _raw_stream(stream, dev)))
+    _check(_lib.seer_qk_norm_rope_backward(ctypes.byref(shape), *[_ref(r) for r in rows[:6]], _ptr(q_weight),
+                                           _ptr(k_weight), _ptr(positions), _ref(rows[6]), _ref(rows[7]),
+                                           _ptr(dq_weight), _ptr(dk_weight), _ptr(num_tokens), _ptr(workspace),
+                                           0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 def dense_decode_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
     shape = DenseShape(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), 0, 1, 0, 0.0)
-    return int(_lib.seer_dense_decode_workspace_bytes(ctypes.addressof(shape)))
+    return int(_lib.seer_dense_decode_workspace_bytes(ctypes.byref(shape)))
 
 
 def alloc_dense_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
@@ -917,53 +885,46 @@ def dense_decode(q: torch.Tensor, k: KVCache, v: KVCache, seqlens: torch.Tensor,
     """Attention of one new token per sequence over its whole cache, or its last `window` tokens (see
     seer_dense_decode).  q and out [B, Hq, d]; k and v of the same type (bf16 or fp16), contiguous or paged with
     pages of any size."""
+    status = _call.dense_decode(q, k._keep, v._keep, seqlens, out, workspace, window, softmax_scale, lse, err, stream)
+    if status >= 0:
+        return _check(status)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D [B, Hq, d] tensor")
-    B, Hq, d = q.shape
-    dt, page, H = q.dtype, 0, 0
+    B, Hq, d = (int(x) for x in q.shape)
+    heads, pages = [], []
     for c, name in ((k, "k"), (v, "v")):
-        shape = c._keep[0].shape
-        if len(shape) != 4 or shape[3] != d:
-            raise ValueError(f"{name}: rows of {d} channels are needed, got {tuple(shape)}")
-        if c.dtype != dt:
-            raise TypeError(f"{name} must be {dt}, got {c.dtype}")
-        if H and shape[1] != H:
-            raise ValueError(f"k has {H} heads, v {shape[1]}")
-        H = shape[1]
+        t = c._keep[0]
+        if t.dim() != 4 or t.shape[3] != d:
+            raise ValueError(f"{name}: rows of {d} channels are needed, got {tuple(t.shape)}")
+        if c.dtype != q.dtype:
+            raise TypeError(f"{name} must be {q.dtype}, got {c.dtype}")
+        heads.append(int(t.shape[1]))
         if c.desc.layout == KV_PAGED:
-            if page and shape[2] != page:
-                raise ValueError(f"k has pages of {page} tokens, v of {shape[2]}")
-            page = shape[2]
-            table = c._keep[1].shape
-            if len(table) != 2 or table[0] < B:
-                raise ValueError(f"{name}: a block table of {B} rows is needed, got {tuple(table)}")
-        elif shape[0] < B:
-            raise ValueError(f"{name}: a cache of {B} sequences is needed, got {tuple(shape)}")
-    dev = _on_current(q)
-    if not (dev >= 0 and q.is_contiguous() and dt in (torch.bfloat16, torch.float16) and isinstance(seqlens, torch.Tensor)
-            and _fits(seqlens, (B,), torch.int32, dev) and isinstance(out, torch.Tensor) and _fits(out, (B, Hq, d), dt, dev)
-            and isinstance(workspace, torch.Tensor) and _fits(workspace, workspace.shape, torch.uint8, dev)
-            and (lse is None or isinstance(lse, torch.Tensor) and _fits(lse, (B, Hq), torch.float32, dev))):
-        _need_shape(seqlens, (B,), "seqlens")
-        _need_shape(out, (B, Hq, d), "out")
-        if lse is not None:
-            _need_shape(lse, (B, Hq), "lse")
-        _need_err(err)
-        if dt not in (torch.bfloat16, torch.float16):
-            raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {dt}")
-        for t, want, name in ((q, dt, "q"), (seqlens, torch.int32, "seqlens"), (out, dt, "out"),
-                              (workspace, torch.uint8, "workspace")):
-            _need(t, want, name)
-        if lse is not None:
-            _need(lse, torch.float32, "lse")
+            pages.append(int(t.shape[2]))
+            if c._keep[1].dim() != 2 or c._keep[1].shape[0] < B:
+                raise ValueError(f"{name}: a block table of {B} rows is needed, got {tuple(c._keep[1].shape)}")
+        elif t.shape[0] < B:
+            raise ValueError(f"{name}: a cache of {B} sequences is needed, got {tuple(t.shape)}")
+    if heads[0] != heads[1]:
+        raise ValueError(f"k has {heads[0]} heads, v {heads[1]}")
+    if len(set(pages)) > 1:
+        raise ValueError(f"k has pages of {pages[0]} tokens, v of {pages[1]}")
+    _need_shape(seqlens, (B,), "seqlens")
+    _need_shape(out, (B, Hq, d), "out")
+    if lse is not None:
+        _need_shape(lse, (B, Hq), "lse")
     _need_err(err)
-    for c, name in ((k, "k"), (v, "v")):
-        if c._keep[0].get_device() != dev:
-            _need_current_device(c._keep[0], name)
-    _pack_dense.pack_into(_scratch.dense, 0, B, Hq, H, d, DTYPES[dt], page or 1, window, softmax_scale)
-    _check(_lib.seer_dense_decode(_scratch.dense_at, q.data_ptr(), ctypes.addressof(k.desc), ctypes.addressof(v.desc),
-                                  seqlens.data_ptr(), out.data_ptr(), _address(lse), workspace.data_ptr(),
-                                  workspace.numel(), _address(err), _raw_stream(stream, dev)))
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q must be torch.bfloat16 or torch.float16, got {q.dtype}")
+    for t, dt, name in ((q, q.dtype, "q"), (seqlens, torch.int32, "seqlens"), (out, q.dtype, "out"),
+                        (workspace, torch.uint8, "workspace")):
+        _need(t, dt, name)
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+    shape = DenseShape(B, Hq, heads[0], d, DTYPES[q.dtype], pages[0] if pages else 1, int(window), float(softmax_scale))
+    _check(_lib.seer_dense_decode(ctypes.byref(shape), _ptr(q), ctypes.byref(k.desc), ctypes.byref(v.desc),
+                                  _ptr(seqlens), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _ptr(err),
+                                  _stream(stream)))
 
 
 class DecodeStep:

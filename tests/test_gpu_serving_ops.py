@@ -601,3 +601,75 @@ def test_serving_steps_together():
         pkg.sparse_decode(sh, qo, K, V, idx, i32([[n] * H for n in nb]), L, sparse, sws, lse=slse)
         R.close(sparse, out.double(), 2 * bo + 2 * R.half_step(dt) * out.double().abs(), "gated, all blocks")
         assert ((slse - lse).abs() <= 2e-3).all()
+
+
+def test_call_layer_and_named_checks_agree(monkeypatch):
+    """Every operator through the compiled call layer, then through the binding's own checks: the same results; and the
+    call layer takes the well-formed calls itself."""
+    pkg = S()
+    from block_sparse_attention_attngate_b200 import seer
+    gn = gen(3)
+    T, Hq, H, d, page = 9, 4, 2, 64, 16
+    x = rnd(gn, T, Hq + 2 * H, d, dt=BF16)
+    w, pos = rnd(gn, d, dt=BF16), i32(list(range(T)))
+    taken = []
+
+    class Layer:
+        def __init__(self, use):
+            self.use = use
+
+        def __getattr__(self, name):
+            def call(*a):
+                if not self.use:
+                    return -1
+                taken.append(getattr(real, name)(*a))
+                return taken[-1]
+            return call
+
+    real, results = seer._call, []
+    for use in (True, False):
+        monkeypatch.setattr(seer, "_call", Layer(use))
+        L, T2, F, C = i32([3, 0]), i32([[5, -1], [-1, -1]]), i32([2, 4, 1, 0, 3, -1]), i32([5])
+        cu, slots, ps, err = i32([0] * 3), i32([0] * 40), i32([0] * 40), i32([0])
+        pkg.page_plan(page, L, i32([20, 5]), T2, F, C, cu, slots, ps, err=err)
+        qo, ko = torch.empty(T, Hq, d, dtype=BF16, device="cuda"), torch.empty(T, H, d, dtype=BF16, device="cuda")
+        kc, vc = (torch.zeros(6, H, page, d, dtype=BF16, device="cuda") for _ in range(2))
+        pkg.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + H], pos, qo, ko, w, w, rope_dim=32, v=x[:, Hq + H:], k_cache=kc,
+                         v_cache=vc, slot_map=slots[:T], num_tokens=i32([T]), err=err)
+        dq, dk, gq, gk = torch.empty_like(qo), torch.empty_like(ko), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+        pkg.qk_norm_rope_backward(qo, ko, x[:, :Hq], x[:, Hq:Hq + H], pos, dq, dk, pkg.alloc_norm_workspace(d), w, w, gq, gk)
+        out, lse = torch.empty(2, Hq, d, dtype=BF16, device="cuda"), torch.empty(2, Hq, device="cuda")
+        pkg.dense_decode(qo[:2], pkg.KVCache.paged(kc, T2), pkg.KVCache.paged(vc, T2), L, out,
+                         pkg.alloc_dense_workspace(2, Hq, H, d), lse=lse, err=err, stream=torch.cuda.current_stream())
+        pkg.page_release(page, L, i32([1, 0]), T2, F, C, err=err)
+        results.append([L, T2, F, C, cu, slots, ps, err, qo, ko, kc, vc, dq, dk, gq, gk, out, lse])
+    assert taken == [0] * 5
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_refusals_on_the_device():
+    """What the call layer does not take is refused by name."""
+    pkg, T, H, d = S(), 4, 2, 64
+    q = torch.zeros(T, H, d, dtype=BF16, device="cuda")
+    pos = i32([0] * T)
+    for bad, exc in ((q.transpose(0, 1).transpose(0, 1)[..., ::2], ValueError), (q.half(), TypeError), (q.cpu(), TypeError),
+                     (q[:3], ValueError)):
+        with pytest.raises(exc):
+            pkg.qk_norm_rope(q, None, pos, bad)
+    with pytest.raises(TypeError):
+        pkg.qk_norm_rope(q, None, pos.long(), torch.empty_like(q))
+    with pytest.raises(pkg.SeerError, match="rope_dim"):
+        pkg.qk_norm_rope(q, None, pos, torch.empty_like(q), rope_dim=24)
+    with pytest.raises(pkg.SeerError, match="share"):
+        pkg.qk_norm_rope(q, None, pos, q, q_nope=q)
+    kv = pkg.KVCache.contiguous(torch.zeros(T, H, 8, d, dtype=BF16, device="cuda"))
+    ws, lens = pkg.alloc_dense_workspace(T, H, H, d), i32([1] * T)
+    with pytest.raises(pkg.SeerError, match="workspace"):
+        pkg.dense_decode(q, kv, kv, lens, torch.empty_like(q), ws[:64])
+    with pytest.raises(pkg.SeerError, match="window"):
+        pkg.dense_decode(q, kv, kv, lens, torch.empty_like(q), ws, window=-1)
+    with pytest.raises(TypeError):
+        pkg.dense_decode(q, kv, kv, lens.float(), torch.empty_like(q), ws)
+    with pytest.raises(TypeError):
+        pkg.dense_decode(q.half(), kv, kv, lens, q.half(), ws)
