@@ -13,12 +13,16 @@
 // between two elements of a thread).
 //
 // Bound: latency (a launch, one round trip for the lengths, one for the page
-// ids, one for the stores); the largest calls write about a megabyte.  One
-// CTA for a decode step; a cluster of eight when more than kOneCtaItems elements are
-// written.  A cluster rather than a plain grid because the lengths may be
-// updated in place: its barrier orders every CTA's reads before rank 0's
-// writes without a second launch or a counter that outlives the call.
+// ids, one for the stores) for a decode step; integer instructions for the
+// largest calls (a megabyte of slots), so divisions by the page size are a
+// multiplication (14 us -> 7.3 us for 131072 tokens of 1024 requests) and the work is shared
+// by up to kMaxCtas CTAs.  When the lengths or the count are updated in place, all reads of them have to
+// come before rank 0's writes: then a cluster of eight, whose barrier orders them without a second launch
+// or a counter that outlives the call.  Small calls run one CTA of kSmall threads (a barrier of 32 warps costs more
+// than their work: 5.7 us -> 3.7 us).
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "seer_device.cuh"
 #include "seer_internal.h"
@@ -26,11 +30,13 @@
 namespace seer {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kPer = kMaxDecodeB / kThreads;   // requests per thread in the scan
-constexpr int kCluster = 8;
+constexpr int kPer = 4;       // requests per thread in the scan
+constexpr int kSmall = 128, kLarge = kMaxDecodeB / kPer;   // threads of a CTA
+constexpr int kCluster = 8, kMaxCtas = 64;
+constexpr int kBatch = 8;   // page ids a thread has on their way at once
 
 // Exclusive scan of two per-thread values over the CTA (totals in *ta, *tb).
+template <int THREADS>
 __device__ __forceinline__ void scan2(long long& a, long long& b, long long* ta, long long* tb, long long (*ws)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long ia = a, ib = b;
@@ -48,7 +54,7 @@ __device__ __forceinline__ void scan2(long long& a, long long& b, long long* ta,
   }
   __syncthreads();
   if (warp == 0) {
-    long long xa = ws[lane][0], xb = ws[lane][1];   // kThreads / 32 == 32 warps
+    long long xa = lane < THREADS / 32 ? ws[lane][0] : 0, xb = lane < THREADS / 32 ? ws[lane][1] : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long ya = __shfl_up_sync(0xffffffffu, xa, off), yb = __shfl_up_sync(0xffffffffu, xb, off);
@@ -57,13 +63,15 @@ __device__ __forceinline__ void scan2(long long& a, long long& b, long long* ta,
         xb += yb;
       }
     }
-    ws[lane][0] = xa;
-    ws[lane][1] = xb;
+    if (lane < THREADS / 32) {
+      ws[lane][0] = xa;
+      ws[lane][1] = xb;
+    }
   }
   __syncthreads();
   const long long ba = warp ? ws[warp - 1][0] : 0, bb = warp ? ws[warp - 1][1] : 0;
-  *ta = ws[31][0];
-  *tb = ws[31][1];
+  *ta = ws[THREADS / 32 - 1][0];
+  *tb = ws[THREADS / 32 - 1][1];
   a = ba + ia - a;
   b = bb + ib - b;
 }
@@ -80,20 +88,28 @@ __device__ __forceinline__ int row_of(const int* first, int n, int x) {
 }
 
 // Elements [lo, hi) of n that this warp handles: equal runs over all warps, whole steps of 32.
+template <int THREADS>
 __device__ __forceinline__ void warp_run(int n, int* lo, int* hi) {
-  const int warps = gridDim.x * (kThreads / 32), w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int warps = gridDim.x * (THREADS / 32), w = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
   const int run = ((n - 1) / (warps * 32) + 1) * 32;   // n >= 1
   const long long at = (long long)w * run;
   *lo = (int)(at < n ? at : n);
   *hi = n - *lo < run ? n : *lo + run;
 }
 
-__device__ __forceinline__ int div_up(int x, int page) { return x / page + (x % page != 0 ? 1 : 0); }
+// x / page for 0 <= x < 2^31, and rounded up
+__device__ __forceinline__ int div(const PageParams& p, int x) {
+  return p.page == 1 ? x : (int)(__umulhi((uint32_t)x, p.magic) >> p.shift);
+}
+__device__ __forceinline__ int div_up(const PageParams& p, int x) {
+  const int q = div(p, x);
+  return q + (x - q * p.page != 0 ? 1 : 0);
+}
 
 // The requests of this thread in the scan: kPer consecutive ones.  Returns false (to the whole CTA)
 // when a length is out of range.  Fills, in shared memory, the length of every request and the
 // scans of its appended tokens (plan only) and of its pages.
-template <bool PLAN>
+template <bool PLAN, int THREADS>
 __device__ __forceinline__ bool scan_requests(const PageParams& p, int* len, int* tok, int* pag, int* total_tok,
                                               int* total_pag, int* free_count, long long (*ws)[2]) {
   const int F = *p.free_count;
@@ -113,11 +129,11 @@ __device__ __forceinline__ bool scan_requests(const PageParams& p, int* len, int
   for (int j = 0; j < kPer; ++j) {
     own[j] = 0;
     if (PLAN) {
-      const long long room = (long long)p.width * p.page;
+      const long long room = min((long long)p.width * p.page, (long long)INT32_MAX);
       const bool ok = L[j] >= 0 && n[j] >= 0 && (long long)L[j] + n[j] <= room;
       bad |= !ok;
       if (ok) {
-        own[j] = div_up(L[j] + n[j], p.page) - div_up(L[j], p.page);
+        own[j] = div_up(p, L[j] + n[j]) - div_up(p, L[j]);
         st += n[j];
         sp += own[j];
       }
@@ -125,13 +141,13 @@ __device__ __forceinline__ bool scan_requests(const PageParams& p, int* len, int
       const bool ok = L[j] >= 0 && L[j] <= (long long)p.width * p.page;
       bad |= !ok;
       if (ok) {
-        own[j] = div_up(L[j], p.page);
+        own[j] = div_up(p, L[j]);
         sp += own[j];
       }
     }
   }
   long long tt, tp;
-  scan2(st, sp, &tt, &tp, ws);
+  scan2<THREADS>(st, sp, &tt, &tp, ws);
   if (PLAN) bad |= tt > p.max_tokens || tp > F;
   else bad |= tp > p.num_pages - (long long)F;
   // totals below 2^31 from here on (max_tokens and num_pages are); on a bad call nothing below is used
@@ -154,19 +170,20 @@ __device__ __forceinline__ bool scan_requests(const PageParams& p, int* len, int
   return __syncthreads_or(bad) == 0;
 }
 
-__global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) page_plan_kernel(const PageParams p) {
   extern __shared__ int sm[];
   __shared__ long long ws[32][2];
   int *len = sm, *tok = sm + p.B, *pag = sm + 2 * p.B;
   const int B = p.B, page = p.page, pages = p.num_pages;
-  const int gt = blockIdx.x * kThreads + threadIdx.x, gn = gridDim.x * kThreads;
+  const int gt = blockIdx.x * THREADS + threadIdx.x, gn = gridDim.x * THREADS;
   pdl_wait();
   pdl_trigger();
   int T, A, F;
-  const bool ok = scan_requests<true>(p, len, tok, pag, &T, &A, &F, ws);
-  if (gridDim.x > 1) cooperative_groups::this_cluster().sync();   // every CTA has read what rank 0 now writes
+  const bool ok = scan_requests<true, THREADS>(p, len, tok, pag, &T, &A, &F, ws);
+  if (p.in_place && gridDim.x > 1) cooperative_groups::this_cluster().sync();   // every CTA has read what rank 0 now writes
   if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < B; b += kThreads) {
+    for (int b = threadIdx.x; b < B; b += THREADS) {
       // bounded: requests in range sum to at most max_tokens
       const int n = ok ? (b + 1 < B ? tok[b + 1] : T) - tok[b] : 0;
       p.seqlens_out[b] = len[b] + n;
@@ -183,31 +200,49 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
   int lo, hi;
   // new pages: element i is page i - A_b of request b
   if (A > 0) {
-    warp_run(A, &lo, &hi);
+    warp_run<THREADS>(A, &lo, &hi);
     int b = lo + lane < hi ? row_of(pag, B, lo + lane) : 0;
-    for (int i = lo + lane; i < hi; i += 32) {
-      while (b + 1 < B && pag[b + 1] <= i) ++b;
-      int id = p.free_list[F - 1 - i];
-      if (id < 0 || id >= pages) {
-        report(p.err, SEER_DEVERR_PAGE_INDEX);
-        id = -1;
+    for (int i0 = lo + lane; i0 < hi; i0 += 32 * kBatch) {
+      int id[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) id[k] = i0 + 32 * k < hi ? p.free_list[F - 1 - (i0 + 32 * k)] : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + 32 * k;
+        if (i >= hi) break;
+        while (b + 1 < B && pag[b + 1] <= i) ++b;
+        const bool good = id[k] >= 0 && id[k] < pages;
+        if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
+        p.block_table[(size_t)b * p.width + div_up(p, len[b]) + (i - pag[b])] = good ? id[k] : -1;
       }
-      p.block_table[(size_t)b * p.width + div_up(len[b], page) + (i - pag[b])] = id;
     }
   }
   // appended tokens; a page that is new in this call is read from the stack, not from the table
   if (T > 0) {
-    warp_run(T, &lo, &hi);
+    warp_run<THREADS>(T, &lo, &hi);
     int b = lo + lane < hi ? row_of(tok, B, lo + lane) : 0;
-    for (int t = lo + lane; t < hi; t += 32) {
-      while (b + 1 < B && tok[b + 1] <= t) ++b;
-      const int L = len[b], pos = L + (t - tok[b]);
-      const int at = pos / page, own = div_up(L, page);
-      const int id = at < own ? p.block_table[(size_t)b * p.width + at] : p.free_list[F - 1 - (pag[b] + at - own)];
-      const bool good = id >= 0 && id < pages;
-      if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
-      p.slot_map[t] = good ? id * page + (pos - at * page) : -1;
-      p.positions[t] = pos;
+    for (int t0 = lo + lane; t0 < hi; t0 += 32 * kBatch) {
+      int id[kBatch], pos[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int t = t0 + 32 * k;
+        id[k] = pos[k] = 0;
+        if (t < hi) {
+          while (b + 1 < B && tok[b + 1] <= t) ++b;
+          pos[k] = len[b] + (t - tok[b]);
+          const int at = div(p, pos[k]), own = div_up(p, len[b]);
+          id[k] = *(at < own ? p.block_table + (size_t)b * p.width + at : p.free_list + (F - 1 - (pag[b] + at - own)));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int t = t0 + 32 * k;
+        if (t >= hi) break;
+        const bool good = id[k] >= 0 && id[k] < pages;
+        if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
+        p.slot_map[t] = good ? id[k] * page + (pos[k] - div(p, pos[k]) * page) : -1;
+        p.positions[t] = pos[k];
+      }
     }
   }
   for (int t = T + gt; t < p.max_tokens; t += gn) {
@@ -216,7 +251,8 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
   }
 }
 
-__global__ void __launch_bounds__(kThreads) page_release_kernel(const PageParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) page_release_kernel(const PageParams p) {
   extern __shared__ int sm[];
   __shared__ long long ws[32][2];
   int *len = sm, *pag = sm + p.B;
@@ -224,10 +260,10 @@ __global__ void __launch_bounds__(kThreads) page_release_kernel(const PageParams
   pdl_wait();
   pdl_trigger();
   int T, A, F;
-  const bool ok = scan_requests<false>(p, len, nullptr, pag, &T, &A, &F, ws);
-  if (gridDim.x > 1) cooperative_groups::this_cluster().sync();   // every CTA has read what rank 0 now writes
+  const bool ok = scan_requests<false, THREADS>(p, len, nullptr, pag, &T, &A, &F, ws);
+  if (p.in_place && gridDim.x > 1) cooperative_groups::this_cluster().sync();   // every CTA has read what rank 0 now writes
   if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < B; b += kThreads)
+    for (int b = threadIdx.x; b < B; b += THREADS)
       p.seqlens_out[b] = ok && p.per_request[b] != 0 ? 0 : len[b];
     if (threadIdx.x == 0) {
       *p.free_count_out = ok ? F + A : F;
@@ -236,30 +272,60 @@ __global__ void __launch_bounds__(kThreads) page_release_kernel(const PageParams
   }
   if (!ok || A == 0) return;
   int lo, hi;
-  warp_run(A, &lo, &hi);
+  warp_run<THREADS>(A, &lo, &hi);
   const int first = lo + (threadIdx.x & 31);
   int b = first < hi ? row_of(pag, B, first) : 0;
-  for (int i = first; i < hi; i += 32) {
-    while (b + 1 < B && pag[b + 1] <= i) ++b;
-    int id = p.block_table[(size_t)b * p.width + (i - pag[b])];
-    if (id < 0 || id >= p.num_pages) {
-      report(p.err, SEER_DEVERR_PAGE_INDEX);
-      id = -1;
+  for (int i0 = first; i0 < hi; i0 += 32 * kBatch) {
+    int id[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k;
+      id[k] = 0;
+      if (i < hi) {
+        while (b + 1 < B && pag[b + 1] <= i) ++b;
+        id[k] = p.block_table[(size_t)b * p.width + (i - pag[b])];
+      }
     }
-    p.free_out[F + i] = id;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + 32 * k >= hi) break;
+      const bool good = id[k] >= 0 && id[k] < p.num_pages;
+      if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
+      p.free_out[F + i0 + 32 * k] = good ? id[k] : -1;
+    }
   }
 }
 
 std::atomic<uint64_t> g_limit[2];
 
-cudaError_t launch(void (*kern)(const PageParams), const PageParams& p, int ctas, size_t smem, std::atomic<uint64_t>& done,
-                   cudaStream_t s) {
-  cudaError_t e = ensure_smem_limit(kern, 3 * kMaxDecodeB * (int)sizeof(int), done);
+// Multiplier and shift with floor(x / d) = mulhi(x, magic) >> shift for 0 <= x < 2^31 and 2 <= d < 2^31: with
+// s = ceil(log2 d) and magic = ceil(2^(31 + s) / d) < 2^32, the excess e = magic d - 2^(31 + s) is below d <= 2^s, so
+// x e < 2^(31 + s) and x magic / 2^(31 + s) stays below the next multiple of 1 / d.  mulhi takes 32 of the 31 + s bits.
+void set_divisor(PageParams& p) {
+  p.magic = 0;
+  p.shift = 0;
+  if (p.page < 2) return;
+  int s = 0;
+  while (((int64_t)1 << s) < p.page) ++s;
+  p.magic = (uint32_t)((((uint64_t)1 << (31 + s)) + p.page - 1) / p.page);
+  p.shift = s - 1;
+}
+
+// arrays: of p.B ints in shared memory; items: elements to write, at most
+cudaError_t launch(void (*small)(const PageParams), void (*large)(const PageParams), PageParams p, int arrays,
+                   int64_t items, std::atomic<uint64_t>& done, cudaStream_t s) {
+  set_divisor(p);
+  p.in_place = p.seqlens == p.seqlens_out || p.free_count == p.free_count_out;
+  const bool one = p.B <= kSmall * kPer && items <= 8 * kSmall;
+  int ctas = 1;
+  if (!one && items > 4 * kLarge)
+    ctas = p.in_place ? kCluster : (int)std::min<int64_t>(kMaxCtas, (items + 2 * kLarge - 1) / (2 * kLarge));
+  cudaError_t e = ensure_smem_limit(large, 3 * kMaxDecodeB * (int)sizeof(int), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(one ? kSmall : kLarge);
+  cfg.dynamicSmemBytes = (size_t)arrays * p.B * sizeof(int);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -268,25 +334,20 @@ cudaError_t launch(void (*kern)(const PageParams), const PageParams& p, int ctas
   attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  cfg.numAttrs = p.in_place && ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, one ? small : large, p);
 }
-
-// Elements written by one CTA before eight share them.
-constexpr int kOneCtaItems = 4 * kThreads;
 
 }  // namespace
 
 cudaError_t launch_page_plan(const PageParams& p, cudaStream_t s) {
-  return launch(page_plan_kernel, p, p.max_tokens > kOneCtaItems ? kCluster : 1, 3 * (size_t)p.B * sizeof(int),
-                g_limit[0], s);
+  return launch(page_plan_kernel<kSmall>, page_plan_kernel<kLarge>, p, 3, p.max_tokens, g_limit[0], s);
 }
 
 cudaError_t launch_page_release(const PageParams& p, cudaStream_t s) {
   // the host does not know how many pages come back; the pool bounds it
-  const int64_t most = (int64_t)p.B * p.width;
-  return launch(page_release_kernel, p, (most < p.num_pages ? most : p.num_pages) > kOneCtaItems ? kCluster : 1,
-                2 * (size_t)p.B * sizeof(int), g_limit[1], s);
+  return launch(page_release_kernel<kSmall>, page_release_kernel<kLarge>, p, 2,
+                std::min<int64_t>((int64_t)p.B * p.width, p.num_pages), g_limit[1], s);
 }
 
 }  // namespace seer

@@ -249,6 +249,8 @@ struct PageParams {
   int32_t* positions;           // [max_tokens]
   int32_t B, page, num_pages, width, max_tokens;
   int32_t* err;
+  uint32_t magic;               // division by the page size; set by the launch, as the rest
+  int32_t shift, in_place;
 };
 cudaError_t launch_page_plan(const PageParams& p, cudaStream_t s);
 cudaError_t launch_page_release(const PageParams& p, cudaStream_t s);

@@ -53,7 +53,7 @@ def pages_problem(seed, B, page, high, new_high, spare, width=None):
     return lens, new, table, free, len(ids) - at, width
 
 
-PLANS = [(1, 64, 200, 3, 0), (1, 1, 5, 4, 2), (3, 16, 100, 40, 1), (33, 7, 50, 9, 5), (500, 16, 300, 20, 3),
+PLANS = [(200, 16, 400, 300, 7), (1, 64, 200, 3, 0), (1, 1, 5, 4, 2), (3, 16, 100, 40, 1), (33, 7, 50, 9, 5), (500, 16, 300, 20, 3),
          (1025, 48, 100, 2, 0), (4096, 16, 40, 3, 11), (64, 128, 4000, 400, 9)]
 
 
@@ -142,6 +142,22 @@ def test_page_release_all_or_nothing(what):
     pkg.page_release(page, L, i32(done), i32(table), F, C, err=err)
     assert int(err) == pkg.DEVERR_COUNT
     assert L.tolist() == lens and F.tolist() == free and int(C) == count
+
+
+def test_page_plan_lengths_past_31_bits():
+    """A table wide enough for more than 2^31 tokens: a length that would pass them is refused as a whole."""
+    pkg, page, T = S(), 1 << 29, i32([[0, 1, 2, 3, 4, 5, 6, 7], [-1] * 8])
+    for lens, new, ok in (([2 ** 31 - 6, 0], [5, 3], True), ([2 ** 31 - 6, 0], [6, 3], False)):
+        L, C, err, table = i32(lens), i32([1]), i32([0]), T.clone()
+        cu, slots, pos = i32([0] * 3), i32([7] * 12), i32([7] * 12)
+        pkg.page_plan(page, L, i32(new), table, i32([2, 1, 0]), C, cu, slots, pos, err=err)
+        if not ok:
+            assert int(err) == pkg.DEVERR_COUNT and L.tolist() == lens and table.tolist() == T.tolist()
+            assert slots.tolist() == [-1] * 12
+            continue
+        # the first row's tokens lie in its page 3, which is outside the pool of 3
+        assert int(err) == pkg.DEVERR_PAGE_INDEX and L.tolist() == [2 ** 31 - 1, 3] and table[1, 0] == 2
+        assert slots.tolist() == [-1] * 5 + [2 * page, 2 * page + 1, 2 * page + 2] + [-1] * 4
 
 
 def test_page_ids_outside_the_pool():
