@@ -10,16 +10,15 @@
 // Bound: HBM -- every key and value is read once; 4 g flops a byte pair at most, a
 // tenth of what the warp-level tensor instructions sustain.
 //
-// Split.  The sequences' tokens in steps of kDenseUnit are one long axis; G
-// ranges of it, times the KV heads, are the work of as many independent warps
-// (one wave, eight to an SM).  A warp walks its range through a ring of
-// shared-memory stages that it fills itself (cp.async, kStages - 1 stages
-// ahead), so the loads never stop at the end of a sequence and no warp waits for
-// another: there is no barrier past the prologue.  The KV heads of a range run
-// at the same time on neighbouring SMs, so a token-major cache's rows are read
-// whole within a short time.  cp.async of 16-byte chunks takes any page size
-// and stride: tokens that are out of range or on a bad page are filled
+// Split.  The rows' (sequence, KV head) tokens in units of kDenseUnit are one long axis; equal ranges of it are the work
+// of as many teams, one wave.  A team's warps take its steps of 4 KB of keys and 4 KB of values in turn, each through a ring
+// of shared-memory slots that it fills itself (cp.async, kSlots - 1 slots ahead, on across the ends of rows).  No
+// warp waits for another but at the end of a row.  cp.async of 16-byte chunks takes any page
+// size and stride: tokens that are out of range or on a bad page are filled
 // with zeros and masked, whatever lies there.
+// A team is a CTA when rows are few (the CTA's warps merge their parts of a row in shared memory, so that a row leaves
+// few pieces), and a single warp when there are kTeamRows rows an SM and more (a barrier a row would cost more
+// than the pieces).
 //
 // Products.  Both are taken transposed so that 16 tokens (or 16 channels) fill the
 // long side of the 16x8x16 instruction and the group's heads the short one (eight a
@@ -28,8 +27,7 @@
 // 8x8 register transpose each.  A lane then holds the same two heads' columns in S, m, l and O.
 //
 // A row that lies in one range is finished there; the pieces of the others go to
-// the workspace in register order, and the join kernel (one warp per eight or
-// fewer pieces, sixteen warps a CTA) merges them.
+// the workspace in register order, and the join kernel merges them.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -41,14 +39,17 @@
 namespace seer {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12, kSlots = 3;   // of a CTA, of a warp's ring
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kStageBytes = 4096;          // K (or V) of one stage
+constexpr int kTeamRows = 6;             // rows an SM from which on teams are single warps
+constexpr int kMinUnits = 4;             // of a CTA's range
+constexpr int kSlotBytes = 4096;   // keys or values of one step
+constexpr int kMaskSteps = 4;      // steps whose masks are kept: more than are in the ring
+static_assert(kMaskSteps > (kSlots + 1) / 2, "a mask outlives its step");
 constexpr int kJoinWarps = 16;
 
 template <int D>
-constexpr int stage_tokens() { return kStageBytes / (2 * D); }   // 16 (d = 128) or 32 (d = 64)
+constexpr int step_tokens() { return kSlotBytes / (2 * D); }   // 16 (d = 128) or 32 (d = 64)
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
@@ -98,33 +99,48 @@ __device__ __forceinline__ int units_of(const DenseParams& p, int len) {
   return (hi - lo + kDenseUnit - 1) / kDenseUnit;
 }
 
-// Position of a warp in its range: the stage of sequence b that starts at token t.
-struct Cursor {
-  int b, t, end;   // end: first token of the sequence that is not this range's
-  int lo;          // first token of the sequence that is seen
+// A range's part of one row: tokens [t0, t1) of sequence b, KV head h.
+struct Part {
+  int b, h;
+  int first, units;   // of the whole row, on the axis of all rows' units
+  int t0, t1;
 };
 
-// Move to the first token of unit u (u < total) of a range that ends at unit u1.
-__device__ __forceinline__ void seek(const DenseParams& p, const int* pre, const int* len, int b, int u, int u1,
-                                     Cursor* c) {
+__device__ __forceinline__ void clip(const DenseParams& p, const int* len, int u0, int u1, Part* r) {
   int lo, hi;
-  token_range(p, len[b], &lo, &hi);
-  c->b = b;
-  c->lo = lo;
-  c->t = lo + (u - pre[b]) * kDenseUnit;
-  const int last = u1 - pre[b];   // units of this sequence up to the range's end
-  c->end = pre[b + 1] <= u1 ? hi : lo + last * kDenseUnit;
+  token_range(p, len[r->b], &lo, &hi);
+  const int skip = max(u0 - r->first, 0), left = u1 - r->first;
+  r->t0 = lo + skip * kDenseUnit;
+  r->t1 = left >= r->units ? hi : lo + left * kDenseUnit;
 }
 
-// Next stage of TS tokens; at a sequence's end the next one that is not empty.  False at the range's end.
-template <int TS>
-__device__ __forceinline__ bool advance(const DenseParams& p, const int* pre, const int* len, int u1, Cursor* c) {
-  c->t += TS;
-  if (c->t < c->end) return true;
-  int b = c->b + 1;
-  if (pre[b] >= u1) return false;
-  while (pre[b + 1] == pre[b]) ++b;   // ends: pre[b] < u1 <= total
-  seek(p, pre, len, b, pre[b], u1, c);
+// The part that holds unit u0 < Hkv * pre[B].
+__device__ __forceinline__ void first_part(const DenseParams& p, const int* pre, const int* len, int u0, int u1, Part* r) {
+  // the last sequence that starts at or before u0 (a sequence without units shares its successor's start)
+  int b = 0;
+  for (int hi = p.B; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (pre[mid] * p.Hkv <= u0) b = mid;
+    else hi = mid;
+  }
+  r->b = b;
+  r->units = pre[b + 1] - pre[b];
+  r->h = (u0 - pre[b] * p.Hkv) / r->units;
+  r->first = pre[b] * p.Hkv + r->h * r->units;
+  clip(p, len, u0, u1, r);
+}
+
+// The range's next part; false at its end.
+__device__ __forceinline__ bool next_part(const DenseParams& p, const int* pre, const int* len, int u0, int u1, Part* r) {
+  r->first += r->units;
+  if (r->first >= u1) return false;
+  if (++r->h == p.Hkv) {
+    r->h = 0;
+    do ++r->b;
+    while (pre[r->b + 1] == pre[r->b]);   // ends: first < u1 <= the axis' length
+    r->units = pre[r->b + 1] - pre[r->b];
+  }
+  clip(p, len, u0, u1, r);
   return true;
 }
 
@@ -140,18 +156,34 @@ __device__ __forceinline__ bool locate(const DenseParams& p, const KvPlain& kv, 
   return true;
 }
 
-template <typename T, int D, int NT>
+// Output and log-sum-exp of one head's channels 16 k + quad and + 8 from its sums (log2 domain).
+template <typename T, int D>
+__device__ __forceinline__ void finish(const DenseParams& p, size_t row0, int head, int k, int quad, float2 o, float m, float l) {
+  if (head >= p.g) return;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  uint16_t* out = p.out + (row0 + head) * D + k * 16 + quad;
+  out[0] = round1(o.x * inv, T());
+  out[8] = round1(o.y * inv, T());
+  if (p.lse && k == 0 && quad == 0) p.lse[row0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <typename T, int D, int NT, bool TEAM>
 __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_constant__ DenseParams p) {
-  constexpr int TS = stage_tokens<D>();
-  constexpr int MT = TS / 16;        // token tiles a stage
+  constexpr int TS = step_tokens<D>();
+  constexpr int MT = TS / 16;        // token tiles a step
   constexpr int KS = D / 16;         // channel steps
   constexpr int CPR = D / 8;         // 16-byte chunks a row
   constexpr int RPI = 32 / CPR;      // rows a warp-wide copy covers
+  constexpr int S = TEAM ? kWarps : 1;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t masks[kWarps][kStages];
+  __shared__ uint32_t masks[kWarps][kMaskSteps];
   __shared__ int scan_ws[kWarps];
-  int* pre = reinterpret_cast<int*>(smem + (size_t)kWarps * kStages * 2 * kStageBytes);   // [B + 1]
-  int* len = pre + p.B + 1;                                                              // [B]
+  constexpr int kSets = NT == 1 ? 2 : 1;   // shared memory is full with two of 16 heads
+  __shared__ float2 parts_ml[kSets][TEAM ? kWarps : 1][NT * 8];   // the warps' maxima and sums
+  constexpr int kRing = kWarps * kSlots * kSlotBytes, kParts = TEAM ? kWarps * KS * 512 : 0;
+  float4* parts_o = reinterpret_cast<float4*>(smem + kRing);          // the warps' outputs of one head tile
+  int* pre = reinterpret_cast<int*>(smem + kRing + kParts);            // [B + 1]
+  int* len = pre + p.B + 1;                                            // [B]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, c2 = 2 * (lane & 3);   // row of a tile, first of the lane's two columns
 
@@ -189,10 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
   if (threadIdx.x == 0) pre[p.B] = total;
   __syncthreads();
 
-  const int W = gridDim.x * kWarps;
-  const int gw = warp * gridDim.x + blockIdx.x;     // neighbouring work on neighbouring SMs
-  const int slots = max(W, p.Hkv);
-  const int G = min(max(W / p.Hkv, 1), total);
+  const int W = gridDim.x * kWarps, gw = blockIdx.x * kWarps + warp;
+  const int axis = total * p.Hkv;   // units of all rows
   // rows without a token
   for (int r = gw; r < p.B * p.Hkv; r += W) {
     const int b = r / p.Hkv, h = r - b * p.Hkv;
@@ -200,99 +230,110 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
     uint16_t* o = p.out + ((size_t)b * p.Hq + (size_t)h * p.g) * D;
     for (int i = lane; i < p.g * D; i += 32) o[i] = 0;
     if (p.lse)
-      for (int i = lane; i < p.g; i += 32) p.lse[(size_t)b * p.Hq + h * p.g + i] = __int_as_float(0xff800000);
+      for (int i = lane; i < p.g; i += 32) p.lse[(size_t)b * p.Hq + h * p.g + i] = -INFINITY;
     if (p.by_row && lane == 0) p.join[r] = make_int4(0, 0, 0, 0);
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * kStageBytes;
-  for (int v = gw; v < slots; v += W) {
-    int4 entry = make_int4(0, 0, 0, 0);
-    if (v < G * p.Hkv) {
-      const int grp = v / p.Hkv, h = v - grp * p.Hkv;
-      const int u0 = (int)((int64_t)grp * total / G), u1 = (int)((int64_t)(grp + 1) * total / G);
-      // first sequence: the last one with pre[b] <= u0 (a sequence without units shares its successor's value)
-      int b0 = 0;
-      for (int hi = p.B; hi - b0 > 1;) {
-        const int mid = (b0 + hi) >> 1;
-        if (pre[mid] <= u0) b0 = mid;
-        else hi = mid;
-      }
-      Cursor rd, ld, nx;   // being computed; being requested; whose page ids are on their way
-      seek(p, pre, len, b0, u0, u1, &rd);
+  const uint32_t ring = smem_u32(smem) + warp * kSlots * kSlotBytes;
+  const int team = TEAM ? blockIdx.x : gw, teams = TEAM ? gridDim.x : W;
+  const int G = min(teams, TEAM ? (axis + kMinUnits - 1) / kMinUnits : axis);   // ranges
+  int4 entry = make_int4(0, 0, 0, 0);
+  if (team < G) {
+      const int u0 = (int)((int64_t)team * axis / G), u1 = (int)((int64_t)(team + 1) * axis / G);
+      Part rd, nx;     // being computed; of the next request (whose page ids are on their way)
+      first_part(p, pre, len, u0, u1, &rd);
       nx = rd;
-      bool nx_ok = true;
-      int id_k = 0, id_v = 0;
+      int rj = TEAM ? warp : 0, nj = rj;   // this warp's next step of the part
+      bool nx_ok = true, values = false;   // the next request is of a step's keys, or of the values beside the last keys
+      auto settle = [&]() {   // to the part that holds step nj
+        while (nx_ok && nx.t0 + nj * TS >= nx.t1) {
+          nj -= (nx.t1 - nx.t0 + TS - 1) / TS;
+          nx_ok = next_part(p, pre, len, u0, u1, &nx);
+        }
+      };
+      settle();
+      int id_k = 0, id_v = 0, nstep = 0;
+      uint32_t fill = ring;                // slot of the next request
+      int64_t off_v = 0;                   // values of the last requested keys, one token a lane
+      uint32_t valid = 0;
       auto fetch_ids = [&]() {   // page ids of nx's tokens, one token a lane
-        const int t = nx.t + lane;
-        if (lane < TS && t < nx.end) {
+        const int t = nx.t0 + nj * TS + lane;
+        if (lane < TS && t < nx.t1) {
           if (p.k.paged) id_k = p.k.block_table[(int64_t)nx.b * p.k.max_pages + t / p.page];
           if (p.v.paged) id_v = p.v.block_table[(int64_t)nx.b * p.v.max_pages + t / p.page];
         }
       };
-      auto request = [&](int stage) {   // fill a stage with nx's tokens and move nx on
-        if (nx_ok) {
-          ld = nx;
-          const int t = ld.t + lane;
-          int64_t ok_ = 0, ov_ = 0;
-          bool good = lane < TS && t < ld.end;
+      const int ch = lane % CPR;
+      auto copy = [&](const uint16_t* data, int64_t off) {
+#pragma unroll
+        for (int i = 0; i < TS / RPI; ++i) {
+          const int r = i * RPI + lane / CPR;
+          const int64_t a = __shfl_sync(0xffffffffu, off, r);
+          cp_async16(fill + r * (2 * D) + ((ch ^ (r & 7)) << 4), data + a + ch * 8, (valid >> r) & 1);
+        }
+      };
+      auto request = [&]() {   // fill the next slot: a step's keys, then its values, in turn
+        if (values) {
+          copy(p.v.data, off_v);
+          values = false;
+        } else if (nx_ok) {
+          const int t = nx.t0 + nj * TS + lane;
+          int64_t off_k = 0;
+          off_v = 0;
+          bool good = lane < TS && t < nx.t1;
           if (good) {
-            const bool gk = locate(p, p.k, id_k, ld.b, t, h, &ok_);
-            const bool gv = locate(p, p.v, id_v, ld.b, t, h, &ov_);
+            const bool gk = locate(p, p.k, id_k, nx.b, t, nx.h, &off_k);
+            const bool gv = locate(p, p.v, id_v, nx.b, t, nx.h, &off_v);
             good = gk && gv;
             if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
           }
-          const uint32_t m = __ballot_sync(0xffffffffu, good);
-          if (lane == 0) masks[warp][stage] = m;
-          nx_ok = advance<TS>(p, pre, len, u1, &nx);
+          valid = __ballot_sync(0xffffffffu, good);
+          if (lane == 0) masks[warp][nstep % kMaskSteps] = valid;
+          ++nstep;
+          copy(p.k.data, off_k);
+          values = true;
+          nj += S;
+          settle();
           if (nx_ok) fetch_ids();
-          const uint32_t base = ring + stage * 2 * kStageBytes;
-          const int ch = lane % CPR;
-#pragma unroll
-          for (int i = 0; i < TS / RPI; ++i) {
-            const int r = i * RPI + lane / CPR;
-            const int64_t a = __shfl_sync(0xffffffffu, ok_, r);
-            cp_async16(base + r * (2 * D) + ((ch ^ (r & 7)) << 4), p.k.data + a + ch * 8, (m >> r) & 1);
-          }
-#pragma unroll
-          for (int i = 0; i < TS / RPI; ++i) {
-            const int r = i * RPI + lane / CPR;
-            const int64_t a = __shfl_sync(0xffffffffu, ov_, r);
-            cp_async16(base + kStageBytes + r * (2 * D) + ((ch ^ (r & 7)) << 4), p.v.data + a + ch * 8, (m >> r) & 1);
-          }
         }
-        cp_commit();   // one group a stage, empty behind the range's end
+        cp_commit();   // one group a slot, empty behind the range's end
+        fill = fill == ring + (kSlots - 1) * kSlotBytes ? ring : fill + kSlotBytes;
       };
-      fetch_ids();
+      if (nx_ok) fetch_ids();
 #pragma unroll
-      for (int s = 0; s < kStages - 1; ++s) request(s);
+      for (int s = 0; s < kSlots - 1; ++s) request();
 
       uint32_t q[NT][KS][2];
       float o[NT][KS][4], m[NT][2], l[NT][2];
-      int stage = 0;
-      bool fresh = true;   // rd stands at the first stage of a sequence's part
-      bool more = true;
-      while (more) {
-        if (fresh) {
-          fresh = false;
+      int step = 0;
+      uint32_t take = ring;   // slot of the next keys or values to compute with
+      int parity = 0;
+      do {   // parts of the range
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int head = n * 8 + quad;
-            const uint16_t* src = p.q + ((size_t)rd.b * p.Hq + (size_t)h * p.g + head) * D + c2;
+        for (int n = 0; n < NT; ++n) {
+          const int head = n * 8 + quad;
+          const uint16_t* src = p.q + ((size_t)rd.b * p.Hq + (size_t)rd.h * p.g + head) * D + c2;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              q[n][k][0] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
-              q[n][k][1] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
-              o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
-            }
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
+          for (int k = 0; k < KS; ++k) {
+            q[n][k][0] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+            q[n][k][1] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+            o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
           }
+          m[n][0] = m[n][1] = -INFINITY;
+          l[n][0] = l[n][1] = 0.f;
         }
-        cp_wait<kStages - 2>();
-        __syncwarp();   // the stage is there for every lane, and every lane is done with the one before
-        request(stage == 0 ? kStages - 1 : stage - 1);
-        const uint32_t kb = ring + stage * 2 * kStageBytes, vb = kb + kStageBytes;
-        const uint32_t mask = masks[warp][stage];
+        for (; rd.t0 + rj * TS < rd.t1; rj += S) {
+        // the next slot has arrived for every lane, and every lane is done with the one before, which is filled again
+        auto next_slot = [&]() {
+          cp_wait<kSlots - 2>();
+          __syncwarp();
+          request();
+          const uint32_t at = take;
+          take = take == ring + (kSlots - 1) * kSlotBytes ? ring : take + kSlotBytes;
+          return at;
+        };
+        const uint32_t kb = next_slot();
+        const uint32_t mask = masks[warp][step % kMaskSteps];
 
         // S^T = K Q^T
         float s[MT][NT][4];
@@ -370,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
         }
 
         // O^T += V^T P^T
+        const uint32_t vb = next_slot();
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -381,14 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
             for (int n = 0; n < NT; ++n) mma(o[n][k], a0, a1, a2, a3, pt[i][n][0], pt[i][n][1], T());
           }
 
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-        const Cursor was = rd;
-        more = advance<TS>(p, pre, len, u1, &rd);
-        if (more && rd.b == was.b) continue;
-        fresh = true;
+        ++step;
+        }
+        rj -= (rd.t1 - rd.t0 + TS - 1) / TS;
 
-        // the range's part of sequence was.b is done
-        const bool head_in = pre[was.b] >= u0, tail_in = pre[was.b + 1] <= u1;
+        // the range's part of the row is done
+        const bool head_in = rd.first >= u0, tail_in = rd.first + rd.units <= u1, whole = head_in && tail_in;
+        const size_t row0 = (size_t)rd.b * p.Hq + (size_t)rd.h * p.g;
+        const int slot = 2 * team + (head_in ? 1 : 0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -397,62 +439,111 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
             l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
             l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
           }
-        if (head_in && tail_in) {
+        if constexpr (TEAM) {
+          // The warps' parts: to the common maximum, then added up by all threads.  With two sets of maxima the next
+          // row's may be written while these are read; with one, the warps wait for the readers.
+          if (quad == 0)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+              parts_ml[parity][warp][n * 8 + c2] = make_float2(m[n][0], l[n][0]);
+              parts_ml[parity][warp][n * 8 + c2 + 1] = make_float2(m[n][1], l[n][1]);
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            __syncthreads();   // the maxima are there (n = 0); the tile before has been added up
+            float f[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int head = n * 8 + c2 + j;
-              if (head >= p.g) continue;
-              const size_t row = (size_t)was.b * p.Hq + (size_t)h * p.g + head;
-              const float inv = l[n][j] == 0.f ? 0.f : 1.0f / l[n][j];
+              float top = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < KS; ++k) {
-                p.out[row * D + k * 16 + quad] = round1(o[n][k][j] * inv, T());
-                p.out[row * D + k * 16 + quad + 8] = round1(o[n][k][j + 2] * inv, T());
-              }
-              if (p.lse && quad == 0) p.lse[row] = l[n][j] == 0.f ? -INFINITY : (m[n][j] + log2f(l[n][j])) * 0.6931471805599453f;
+              for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts_ml[parity][w][n * 8 + c2 + j].x);
+              f[j] = m[n][j] == -INFINITY ? 0.f : exp2f(m[n][j] - top);
             }
-          if (p.by_row && lane == 0) p.join[was.b * p.Hkv + h] = make_int4(0, 1, 0, 0);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+              parts_o[(warp * KS + k) * 32 + lane] =
+                  make_float4(o[n][k][0] * f[0], o[n][k][1] * f[1], o[n][k][2] * f[0], o[n][k][3] * f[1]);
+            __syncthreads();
+            if (threadIdx.x < KS * 32) {
+              const int k = threadIdx.x >> 5;
+              float4 x = parts_o[threadIdx.x];
+#pragma unroll
+              for (int w = 1; w < kWarps; ++w) {
+                const float4 y = parts_o[w * KS * 32 + threadIdx.x];
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+              }
+              float mm[2], ll[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                mm[j] = -INFINITY;
+                ll[j] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mm[j] = fmaxf(mm[j], parts_ml[parity][w][n * 8 + c2 + j].x);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                  const float2 ml = parts_ml[parity][w][n * 8 + c2 + j];
+                  ll[j] += ml.x == -INFINITY ? ml.y : ml.y * exp2f(ml.x - mm[j]);   // 0, or NaN kept
+                }
+              }
+              if (whole) {
+                finish<T, D>(p, row0, n * 8 + c2, k, quad, make_float2(x.x, x.z), mm[0], ll[0]);
+                finish<T, D>(p, row0, n * 8 + c2 + 1, k, quad, make_float2(x.y, x.w), mm[1], ll[1]);
+              } else {
+                p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] = x;
+                if (k == 0 && quad == 0) p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(mm[0], ll[0], mm[1], ll[1]);
+              }
+            }
+          }
+          if (kSets == 2) parity ^= 1;
+          else __syncthreads();
         } else {
-          const int slot = 2 * v + (head_in ? 1 : 0);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-              p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] =
-                  make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
-            if (quad == 0)
+            for (int k = 0; k < KS; ++k) {
+              if (whole) {
+                finish<T, D>(p, row0, n * 8 + c2, k, quad, make_float2(o[n][k][0], o[n][k][2]), m[n][0], l[n][0]);
+                finish<T, D>(p, row0, n * 8 + c2 + 1, k, quad, make_float2(o[n][k][1], o[n][k][3]), m[n][1], l[n][1]);
+              } else {
+                p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] =
+                    make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
+              }
+            }
+            if (!whole && quad == 0)
               p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(m[n][0], l[n][0], m[n][1], l[n][1]);
           }
-          if (head_in) {
-            // last range of the sequence: the one that holds its last unit
-            const int last = (int)((((int64_t)pre[was.b + 1]) * G - 1) / total);
-            entry = make_int4(was.b * p.Hkv + h, last - grp + 1, grp, 0);
-            if (p.by_row && lane == 0) p.join[was.b * p.Hkv + h] = entry;
-          }
         }
-      }
+        if (head_in && lane == 0 && (!TEAM || warp == 0)) {
+          // last range of the row: the one that holds its last unit
+          const int last = (int)(((int64_t)(rd.first + rd.units) * G - 1) / axis);
+          const int4 e = make_int4(rd.b * p.Hkv + rd.h, last - team + 1, team, 0);
+          if (p.by_row) p.join[e.x] = e;
+          else if (!whole) entry = e;
+        }
+      } while (next_part(p, pre, len, u0, u1, &rd));
       cp_wait<0>();
-      __syncwarp();   // the ring is free for the next range
-    }
-    if (!p.by_row && lane == 0) p.join[v] = entry;
   }
+  if (!p.by_row && lane == 0 && (!TEAM || warp == 0)) p.join[team] = entry;
 }
 
-// One CTA per row that lies in several ranges (x) and 16 channels x 8 heads of it (y): its warps take the
-// pieces in turn, then warp 0 merges the warps.
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) dense_join_kernel(const __grid_constant__ DenseParams p) {
+// Joins the rows that lie in several ranges, 16 channels x 8 heads of one at a time.  WIDE: a CTA each, whose warps take
+// the pieces in turn and warp 0 merges the warps (rows of many pieces); else a warp each.
+template <typename T, int D, int NT, bool WIDE>
+__global__ void __launch_bounds__(kJoinWarps * 32) dense_join_kernel(const __grid_constant__ DenseParams p, int entries) {
   constexpr int KS = D / 16;
-  __shared__ float4 so[kJoinWarps][32], sml[kJoinWarps][32];
+  __shared__ float4 so[WIDE ? kJoinWarps : 1][32], sml[WIDE ? kJoinWarps : 1][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = blockIdx.y / KS, k = blockIdx.y - n * KS;
+  const int64_t item = WIDE ? blockIdx.x : (int64_t)blockIdx.x * kJoinWarps + warp;
+  const int at = (int)(item / (NT * KS)), nk = (int)(item - (int64_t)at * (NT * KS));
+  const int n = nk / KS, k = nk - n * KS;
   pdl_wait();
   pdl_trigger();
-  const int4 e = p.join[blockIdx.x];
+  if (at >= entries) return;
+  const int4 e = p.join[at];
   if (e.y < 2) return;
-  const int b = e.x / p.Hkv, h = e.x - b * p.Hkv;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   auto merge = [&](const float4& x, const float4& ml) {
@@ -469,52 +560,60 @@ __global__ void __launch_bounds__(kJoinWarps * 32) dense_join_kernel(const __gri
     m1 = n1;
   };
 #pragma unroll 4
-  for (int i = warp; i < e.y; i += kJoinWarps) {
-    const size_t slot = 2 * ((size_t)(e.z + i) * p.Hkv + h) + (i == 0 ? 1 : 0);
-    merge(p.o_part[(slot * NT * KS + n * KS + k) * 32 + lane], p.ml_part[slot * NT * 4 + n * 4 + (lane & 3)]);
+  for (int i = WIDE ? warp : 0; i < e.y; i += WIDE ? kJoinWarps : 1) {
+    const size_t slot = 2 * (size_t)(e.z + i) + (i == 0 ? 1 : 0);
+    merge(p.o_part[(slot * NT * KS + nk) * 32 + lane], p.ml_part[slot * NT * 4 + n * 4 + (lane & 3)]);
   }
-  so[warp][lane] = o;
-  sml[warp][lane] = make_float4(m0, l0, m1, l1);
-  __syncthreads();
-  if (warp != 0) return;
-  const int used = min(kJoinWarps, e.y);
-  for (int w = 1; w < used; ++w) merge(so[w][lane], sml[w][lane]);
-  const int quad = lane >> 2, head = n * 8 + 2 * (lane & 3);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (head + j >= p.g) continue;
-    const size_t row = (size_t)b * p.Hq + (size_t)h * p.g + head + j;
-    const float l = j ? l1 : l0, mm = j ? m1 : m0, inv = l == 0.f ? 0.f : 1.0f / l;
-    p.out[row * D + k * 16 + quad] = round1((j ? o.y : o.x) * inv, T());
-    p.out[row * D + k * 16 + quad + 8] = round1((j ? o.w : o.z) * inv, T());
-    if (p.lse && k == 0 && quad == 0) p.lse[row] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+  if constexpr (WIDE) {
+    so[warp][lane] = o;
+    sml[warp][lane] = make_float4(m0, l0, m1, l1);
+    __syncthreads();
+    if (warp != 0) return;
+    const int used = min(kJoinWarps, e.y);
+    for (int w = 1; w < used; ++w) merge(so[w][lane], sml[w][lane]);
   }
+  const int b = e.x / p.Hkv, h = e.x - b * p.Hkv, quad = lane >> 2, head = n * 8 + 2 * (lane & 3);
+  const size_t row0 = (size_t)b * p.Hq + (size_t)h * p.g;
+  finish<T, D>(p, row0, head, k, quad, make_float2(o.x, o.z), m0, l0);
+  finish<T, D>(p, row0, head + 1, k, quad, make_float2(o.y, o.w), m1, l1);
 }
 
-std::atomic<uint64_t> g_limit[8];
+std::atomic<uint64_t> g_limit[16];
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool TEAM>
 cudaError_t run(const DenseParams& p, int ctas, cudaStream_t s) {
-  constexpr int ring = kWarps * kStages * 2 * kStageBytes;
-  constexpr int which = (std::is_same<T, __half>::value ? 4 : 0) + (D == 128 ? 2 : 0) + NT - 1;
-  cudaError_t e = ensure_smem_limit(dense_decode_kernel<T, D, NT>, ring + (2 * kMaxDecodeB + 1) * (int)sizeof(int),
+  constexpr int fixed = kWarps * kSlots * kSlotBytes + (TEAM ? kWarps * (D / 16) * 512 : 0);
+  constexpr int which = (std::is_same<T, __half>::value ? 8 : 0) + (D == 128 ? 4 : 0) + (NT - 1) * 2 + (TEAM ? 1 : 0);
+  cudaError_t e = ensure_smem_limit(dense_decode_kernel<T, D, NT, TEAM>, fixed + (2 * kMaxDecodeB + 1) * (int)sizeof(int),
                                     g_limit[which]);
   if (e != cudaSuccess) return e;
-  const size_t smem = ring + (2 * (size_t)p.B + 1) * sizeof(int);
-  if ((e = launch_pdl(dense_decode_kernel<T, D, NT>, dim3(ctas), dim3(kThreads), smem, s, p)) != cudaSuccess) return e;
-  const int rows = p.by_row ? p.B * p.Hkv : dense_ranges(ctas, p.Hkv);
-  return launch_pdl(dense_join_kernel<T, D, NT>, dim3(rows, NT * (D / 16)), dim3(kJoinWarps * 32), 0, s, p);
+  const size_t smem = fixed + (2 * (size_t)p.B + 1) * sizeof(int);
+  e = launch_pdl(dense_decode_kernel<T, D, NT, TEAM>, dim3(ctas), dim3(kThreads), smem, s, p);
+  if (e != cudaSuccess) return e;
+  // a row has about ranges / rows + 1 pieces, at most; a warp takes up to nine
+  const int ranges = dense_ranges(ctas, p.B * p.Hkv), entries = p.by_row ? p.B * p.Hkv : ranges;
+  const int items = entries * NT * (D / 16);
+  if (ranges > 8 * entries)
+    return launch_pdl(dense_join_kernel<T, D, NT, true>, dim3(items), dim3(kJoinWarps * 32), 0, s, p, entries);
+  return launch_pdl(dense_join_kernel<T, D, NT, false>, dim3((items + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, s,
+                    p, entries);
+}
+
+template <typename T, int D>
+cudaError_t run_width(const DenseParams& p, int ctas, cudaStream_t s) {
+  const bool team = dense_ranges(ctas, p.B * p.Hkv) == ctas;
+  if (p.g <= 8) return team ? run<T, D, 1, true>(p, ctas, s) : run<T, D, 1, false>(p, ctas, s);
+  return team ? run<T, D, 2, true>(p, ctas, s) : run<T, D, 2, false>(p, ctas, s);
 }
 
 template <typename T>
 cudaError_t run_type(const DenseParams& p, int D, int ctas, cudaStream_t s) {
-  if (D == 64) return p.g <= 8 ? run<T, 64, 1>(p, ctas, s) : run<T, 64, 2>(p, ctas, s);
-  return p.g <= 8 ? run<T, 128, 1>(p, ctas, s) : run<T, 128, 2>(p, ctas, s);
+  return D == 64 ? run_width<T, 64>(p, ctas, s) : run_width<T, 128>(p, ctas, s);
 }
 
 }  // namespace
 
-int dense_ranges(int ctas, int Hkv) { return std::max(ctas * kWarps, Hkv); }
+int dense_ranges(int ctas, int rows) { return rows >= kTeamRows * ctas ? ctas * kWarps : ctas; }
 
 cudaError_t launch_dense_decode(const DenseParams& p, int D, int dtype, int ctas, cudaStream_t s) {
   return dtype == SEER_BF16 ? run_type<__nv_bfloat16>(p, D, ctas, s) : run_type<__half>(p, D, ctas, s);

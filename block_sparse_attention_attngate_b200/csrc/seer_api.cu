@@ -1214,8 +1214,8 @@ seer_status check_dense(const seer_dense_t* s) {
     return fail(SEER_ERR_UNSUPPORTED, "head_dim %d not in {64, 128}", s->head_dim);
   if (s->dtype != SEER_BF16 && s->dtype != SEER_FP16) return fail(SEER_ERR_UNSUPPORTED, "dtype %d not bf16 or fp16", s->dtype);
   if (s->batch > seer::kMaxDecodeB) return fail(SEER_ERR_UNSUPPORTED, "batch %d > %d", s->batch, seer::kMaxDecodeB);
-  if ((int64_t)s->batch * s->num_kv_heads >= (int64_t)1 << 30)
-    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads must be below 2^30");
+  if ((int64_t)s->batch * s->num_kv_heads >= (int64_t)1 << 24)
+    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads must be below 2^24");
   if (s->window < 0) return fail(SEER_ERR_INVALID_ARG, "window must be >= 0 (0 = all tokens)");
   if (!(s->softmax_scale >= 0.f) || !isfinite(s->softmax_scale))
     return fail(SEER_ERR_INVALID_ARG, "softmax_scale must be >= 0 (0 = 1/sqrt(head_dim))");
@@ -1224,7 +1224,7 @@ seer_status check_dense(const seer_dense_t* s) {
 
 // join entries | {m, l} of the pieces | outputs of the pieces (two pieces a range: its first and last sequence)
 size_t dense_layout(const seer_dense_t* s, int ctas, size_t* off_ml, size_t* off_o) {
-  const size_t ranges = seer::dense_ranges(ctas, s->num_kv_heads);
+  const size_t ranges = seer::dense_ranges(ctas, s->batch * s->num_kv_heads);
   const size_t tiles = s->num_q_heads / s->num_kv_heads > 8 ? 2 : 1;   // of eight heads
   *off_ml = up256(ranges * sizeof(int4));
   *off_o = *off_ml + up256(2 * ranges * tiles * 4 * sizeof(float4));
@@ -1262,8 +1262,8 @@ seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const se
   const bool paged = k->layout == SEER_KV_PAGED || v->layout == SEER_KV_PAGED;
   if (paged && shape->page_size < 1) return fail(SEER_ERR_INVALID_ARG, "page_size must be >= 1");
   const int64_t cap = std::min(kv_capacity(shape, k), kv_capacity(shape, v));
-  if (cap > INT32_MAX - 64 || (int64_t)shape->batch * (cap / 32 + 1) >= (int64_t)1 << 30)
-    return fail(SEER_ERR_UNSUPPORTED, "batch * (cache capacity / 32 + 1) must be below 2^30");
+  if (cap > INT32_MAX - 64 || cap / 32 + 1 >= ((int64_t)1 << 30) / shape->batch / shape->num_kv_heads)
+    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads * (cache capacity / 32 + 1) must be below 2^30");
   int dev;
   DevFacts* df;
   if ((st = device_facts(&dev, &df)) != SEER_OK) return st;
@@ -1291,7 +1291,7 @@ seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const se
   p.join = reinterpret_cast<int4*>(ws);
   p.ml_part = reinterpret_cast<float4*>(ws + off_ml);
   p.o_part = reinterpret_cast<float4*>(ws + off_o);
-  p.by_row = (int64_t)p.B * p.Hkv <= seer::dense_ranges(df->sms, p.Hkv);
+  p.by_row = p.B * p.Hkv <= seer::dense_ranges(df->sms, p.B * p.Hkv);
   p.err = err_word;
   cudaError_t e = seer::launch_dense_decode(p, shape->head_dim, shape->dtype, df->sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dense_decode launch");

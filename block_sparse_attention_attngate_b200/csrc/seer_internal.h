@@ -311,7 +311,7 @@ struct DenseParams {
 };
 constexpr int kDenseMaxGroup = 16;
 constexpr int kDenseUnit = 32;  // tokens per scheduling unit
-int dense_ranges(int ctas, int Hkv);   // (range, KV head) pairs of a launch, at most
+int dense_ranges(int ctas, int rows);   // ranges of a launch over `rows` (sequence, KV head) rows, at most
 cudaError_t launch_dense_decode(const DenseParams& p, int D, int dtype, int ctas, cudaStream_t s);
 
 // Record `msg` as the text seer_last_error() returns on this thread; returns `status`.

@@ -607,9 +607,9 @@ typedef struct {
  *   seqlens    device int32 [B], L_b counting the new token
  *   workspace  device, >= seer_dense_decode_workspace_bytes(shape) bytes, 16-byte aligned, no initial
  *              value needed; calls on one workspace must not overlap on the GPU
- * batch <= 4096, batch * Hkv < 2^30 and batch * (cache capacity / 32 + 1) < 2^30.  Two launches: the split
- * pass, one wave of warps over equal ranges of the sequences' tokens, and the join of the rows that lie
- * in several ranges.  Results do not depend on timing (no atomics).
+ * batch <= 4096, batch * Hkv < 2^24 and batch * Hkv * (cache capacity / 32 + 1) < 2^30.  Two launches:
+ * the split pass, one wave over equal ranges of all rows' tokens, and the join of the rows that lie in
+ * several ranges.  Results do not depend on timing (no atomics).
  */
 size_t seer_dense_decode_workspace_bytes(const seer_dense_t* shape);
 seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const seer_kv_t* k, const seer_kv_t* v,

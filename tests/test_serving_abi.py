@@ -224,7 +224,7 @@ def test_dense_refusals():
     for kw, st, word in ((dict(batch=0), 1, "batch"), (dict(batch=4097), 2, "batch"), (dict(num_q_heads=9), 1, "multiple"),
                          (dict(num_q_heads=34), 2, "group"), (dict(head_dim=80), 2, "head_dim"), (dict(dtype=2), 2, "dtype"),
                          (dict(window=-1), 1, "window"), (dict(softmax_scale=-1.0), 1, "scale"),
-                         (dict(softmax_scale=float("nan")), 1, "scale"), (dict(num_kv_heads=1 << 29, num_q_heads=1 << 29), 2, "2^30")):
+                         (dict(softmax_scale=float("nan")), 1, "scale"), (dict(num_kv_heads=1 << 22, num_q_heads=1 << 22), 2, "2^24")):
         assert dense(**kw) == st and said(word), kw
     assert dense(contiguous(data=4104)) == 1 and said("aligned")
     assert dense(contiguous(stride_t=132)) == 1 and said("strides")
