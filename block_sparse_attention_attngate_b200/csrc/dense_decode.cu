@@ -16,9 +16,9 @@
 // warp waits for another but at the end of a row.  cp.async of 16-byte chunks takes any page
 // size and stride: tokens that are out of range or on a bad page are filled
 // with zeros and masked, whatever lies there.
-// A team is a CTA when rows are few (the CTA's warps merge their parts of a row in shared memory, so that a row leaves
-// few pieces), and a single warp when there are kTeamRows rows an SM and more (a barrier a row would cost more
-// than the pieces).
+// A team is a CTA when the rows are long (its warps merge their parts of a row in shared memory, so that a row leaves few
+// pieces), and a single warp when they are short (a merge costs more than the rows).  A row counts kPad units on top of its
+// own, about what a merge costs, so that ranges of many short rows beside few long ones take alike.
 //
 // Products.  Both are taken transposed so that 16 tokens (or 16 channels) fill the
 // long side of the 16x8x16 instruction and the group's heads the short one (eight a
@@ -41,19 +41,28 @@ namespace {
 
 constexpr int kWarps = 12, kSlots = 3;   // of a CTA, of a warp's ring
 constexpr int kThreads = kWarps * 32;
-constexpr int kTeamRows = 6;             // rows an SM from which on teams are single warps
-constexpr int kMinUnits = 4;             // of a CTA's range
+constexpr int kTeamRows = 6;             // rows an SM from which on teams are single warps whatever the lengths
+constexpr int kTeamUnits = 24;           // units of the mean row from which on teams are CTAs
+constexpr int kPad = 6;
+constexpr int kMinUnits = 4;             // of a range, about
 constexpr int kSlotBytes = 4096;   // keys or values of one step
 constexpr int kMaskSteps = 4;      // steps whose masks are kept: more than are in the ring
 static_assert(kMaskSteps > (kSlots + 1) / 2, "a mask outlives its step");
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32, kNarrowWarps = 8;
+constexpr int kWideRows = 64;            // rows up to which a join takes a CTA for each
 
 template <int D>
 constexpr int step_tokens() { return kSlotBytes / (2 * D); }   // 16 (d = 128) or 32 (d = 64)
 
+// d = 128: a row is 256 bytes, which L2 may fetch at once; d = 64: the next 128 bytes may be another head's.
+template <int D>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-               : "memory");
+  if constexpr (D == 128)
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -102,19 +111,19 @@ __device__ __forceinline__ int units_of(const DenseParams& p, int len) {
 // A range's part of one row: tokens [t0, t1) of sequence b, KV head h.
 struct Part {
   int b, h;
-  int first, units;   // of the whole row, on the axis of all rows' units
+  int first, units;   // of the row's tokens, on the axis (its padding lies before them)
   int t0, t1;
 };
 
 __device__ __forceinline__ void clip(const DenseParams& p, const int* len, int u0, int u1, Part* r) {
   int lo, hi;
   token_range(p, len[r->b], &lo, &hi);
-  const int skip = max(u0 - r->first, 0), left = u1 - r->first;
+  const int skip = max(u0 - r->first, 0), left = max(u1 - r->first, 0);
   r->t0 = lo + skip * kDenseUnit;
   r->t1 = left >= r->units ? hi : lo + left * kDenseUnit;
 }
 
-// The part that holds unit u0 < Hkv * pre[B].
+// The part of the row that unit u0 < Hkv * pre[B] belongs to; empty when the range ends in the row's padding.
 __device__ __forceinline__ void first_part(const DenseParams& p, const int* pre, const int* len, int u0, int u1, Part* r) {
   // the last sequence that starts at or before u0 (a sequence without units shares its successor's start)
   int b = 0;
@@ -123,22 +132,23 @@ __device__ __forceinline__ void first_part(const DenseParams& p, const int* pre,
     if (pre[mid] * p.Hkv <= u0) b = mid;
     else hi = mid;
   }
+  const int span = pre[b + 1] - pre[b];
   r->b = b;
-  r->units = pre[b + 1] - pre[b];
-  r->h = (u0 - pre[b] * p.Hkv) / r->units;
-  r->first = pre[b] * p.Hkv + r->h * r->units;
+  r->units = span - p.pad;
+  r->h = (u0 - pre[b] * p.Hkv) / span;
+  r->first = pre[b] * p.Hkv + r->h * span + p.pad;
   clip(p, len, u0, u1, r);
 }
 
 // The range's next part; false at its end.
 __device__ __forceinline__ bool next_part(const DenseParams& p, const int* pre, const int* len, int u0, int u1, Part* r) {
-  r->first += r->units;
+  r->first += r->units + p.pad;
   if (r->first >= u1) return false;
   if (++r->h == p.Hkv) {
     r->h = 0;
     do ++r->b;
     while (pre[r->b + 1] == pre[r->b]);   // ends: first < u1 <= the axis' length
-    r->units = pre[r->b + 1] - pre[r->b];
+    r->units = pre[r->b + 1] - pre[r->b] - p.pad;
   }
   clip(p, len, u0, u1, r);
   return true;
@@ -167,20 +177,19 @@ __device__ __forceinline__ void finish(const DenseParams& p, size_t row0, int he
   if (p.lse && k == 0 && quad == 0) p.lse[row0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <typename T, int D, int NT, bool TEAM>
+template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_constant__ DenseParams p) {
   constexpr int TS = step_tokens<D>();
   constexpr int MT = TS / 16;        // token tiles a step
   constexpr int KS = D / 16;         // channel steps
   constexpr int CPR = D / 8;         // 16-byte chunks a row
   constexpr int RPI = 32 / CPR;      // rows a warp-wide copy covers
-  constexpr int S = TEAM ? kWarps : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t masks[kWarps][kMaskSteps];
   __shared__ int scan_ws[kWarps];
   constexpr int kSets = NT == 1 ? 2 : 1;   // shared memory is full with two of 16 heads
-  __shared__ float2 parts_ml[kSets][TEAM ? kWarps : 1][NT * 8];   // the warps' maxima and sums
-  constexpr int kRing = kWarps * kSlots * kSlotBytes, kParts = TEAM ? kWarps * KS * 512 : 0;
+  __shared__ float2 parts_ml[kSets][kWarps][NT * 8];   // the warps' maxima and sums
+  constexpr int kRing = kWarps * kSlots * kSlotBytes, kParts = kWarps * KS * 512;
   float4* parts_o = reinterpret_cast<float4*>(smem + kRing);          // the warps' outputs of one head tile
   int* pre = reinterpret_cast<int*>(smem + kRing + kParts);            // [B + 1]
   int* len = pre + p.B + 1;                                            // [B]
@@ -190,39 +199,61 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
   pdl_wait();
   pdl_trigger();
 
-  // exclusive scan of the sequences' units
-  int total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const int L = b < p.B ? p.seqlens[b] : 0;
-    const int n = b < p.B ? units_of(p, L) : 0;
-    if (L > p.cap && blockIdx.x == 0) report(p.err, SEER_DEVERR_COUNT);
-    int inc = n;
+  // exclusive scan of the sequences' units, a row's padding with them
+  int total = 0, filled = 0;   // units of one KV head's rows, rows with tokens
+  auto row_units = [&](int b, int* L) {
+    *L = b < p.B ? p.seqlens[b] : 0;
+    if (*L > p.cap && blockIdx.x == 0) report(p.err, SEER_DEVERR_COUNT);
+    const int n = units_of(p, *L);
+    return n > 0 ? n + p.pad : 0;
+  };
+  auto warp_scan = [&](int x) {   // inclusive
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += x;
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
-    if (lane == 31) scan_ws[warp] = inc;
-    __syncthreads();
-    int before = 0, all = 0;
+    return x;
+  };
+  if (p.B <= 32) {   // every warp for itself: all write the same
+    int L;
+    const int n = row_units(lane, &L), inc = warp_scan(n);
+    if (lane < p.B) {
+      pre[lane] = inc - n;
+      len[lane] = L;
+    }
+    total = __shfl_sync(0xffffffffu, inc, 31);
+    filled = __popc(__ballot_sync(0xffffffffu, n > 0));
+    if (lane == 0) pre[p.B] = total;
+    __syncwarp();
+  } else {
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int L;
+      const int n = row_units(b, &L), inc = warp_scan(n);
+      if (lane == 31) scan_ws[warp] = inc;
+      filled += __syncthreads_count(n > 0);
+      int before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      before += w < warp ? scan_ws[w] : 0;
-      all += scan_ws[w];
+      for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? scan_ws[w] : 0;
+        all += scan_ws[w];
+      }
+      if (b < p.B) {
+        pre[b] = total + before + inc - n;
+        len[b] = L;
+      }
+      total += all;
+      __syncthreads();
     }
-    if (b < p.B) {
-      pre[b] = total + before + inc - n;
-      len[b] = L;
-    }
-    total += all;
+    if (threadIdx.x == 0) pre[p.B] = total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) pre[p.B] = total;
-  __syncthreads();
 
   const int W = gridDim.x * kWarps, gw = blockIdx.x * kWarps + warp;
   const int axis = total * p.Hkv;   // units of all rows
+  const bool wide = p.pad > 0 && total >= filled * (kTeamUnits + kPad);
+  const int S = wide ? kWarps : 1;  // warps of a team
   // rows without a token
   for (int r = gw; r < p.B * p.Hkv; r += W) {
     const int b = r / p.Hkv, h = r - b * p.Hkv;
@@ -235,15 +266,25 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
   }
 
   const uint32_t ring = smem_u32(smem) + warp * kSlots * kSlotBytes;
-  const int team = TEAM ? blockIdx.x : gw, teams = TEAM ? gridDim.x : W;
-  const int G = min(teams, TEAM ? (axis + kMinUnits - 1) / kMinUnits : axis);   // ranges
+  const int team = wide ? blockIdx.x : gw;
+  const int G = min(wide ? gridDim.x : W, (axis + kMinUnits - 1) / kMinUnits);   // ranges
   int4 entry = make_int4(0, 0, 0, 0);
+  int u0 = 0, u1 = 0;
+  Part rd, nx;     // being computed; of the next request (whose page ids are on their way)
+  rd.t0 = rd.t1 = 0;
   if (team < G) {
-      const int u0 = (int)((int64_t)team * axis / G), u1 = (int)((int64_t)(team + 1) * axis / G);
-      Part rd, nx;     // being computed; of the next request (whose page ids are on their way)
-      first_part(p, pre, len, u0, u1, &rd);
+    if (axis < 1 << 20) {   // a 64-bit division takes its time
+      u0 = (int)((uint32_t)team * (uint32_t)axis / (uint32_t)G);
+      u1 = (int)((uint32_t)(team + 1) * (uint32_t)axis / (uint32_t)G);
+    } else {
+      u0 = (int)((int64_t)team * axis / G);
+      u1 = (int)((int64_t)(team + 1) * axis / G);
+    }
+    first_part(p, pre, len, u0, u1, &rd);
+  }
+  if (rd.t0 < rd.t1) {
       nx = rd;
-      int rj = TEAM ? warp : 0, nj = rj;   // this warp's next step of the part
+      int rj = wide ? warp : 0, nj = rj;   // this warp's next step of the part
       bool nx_ok = true, values = false;   // the next request is of a step's keys, or of the values beside the last keys
       auto settle = [&]() {   // to the part that holds step nj
         while (nx_ok && nx.t0 + nj * TS >= nx.t1) {
@@ -269,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
         for (int i = 0; i < TS / RPI; ++i) {
           const int r = i * RPI + lane / CPR;
           const int64_t a = __shfl_sync(0xffffffffu, off, r);
-          cp_async16(fill + r * (2 * D) + ((ch ^ (r & 7)) << 4), data + a + ch * 8, (valid >> r) & 1);
+          cp_async16<D>(fill + r * (2 * D) + ((ch ^ (r & 7)) << 4), data + a + ch * 8, (valid >> r) & 1);
         }
       };
       auto request = [&]() {   // fill the next slot: a step's keys, then its values, in turn
@@ -439,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
             l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
             l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
           }
-        if constexpr (TEAM) {
+        if (wide) {
           // The warps' parts: to the common maximum, then added up by all threads.  With two sets of maxima the next
           // row's may be written while these are read; with one, the warps wait for the readers.
           if (quad == 0)
@@ -516,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
               p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(m[n][0], l[n][0], m[n][1], l[n][1]);
           }
         }
-        if (head_in && lane == 0 && (!TEAM || warp == 0)) {
+        if (head_in && lane == 0 && (!wide || warp == 0)) {
           // last range of the row: the one that holds its last unit
           const int last = (int)(((int64_t)(rd.first + rd.units) * G - 1) / axis);
           const int4 e = make_int4(rd.b * p.Hkv + rd.h, last - team + 1, team, 0);
@@ -526,18 +567,20 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
       } while (next_part(p, pre, len, u0, u1, &rd));
       cp_wait<0>();
   }
-  if (!p.by_row && lane == 0 && (!TEAM || warp == 0)) p.join[team] = entry;
+  if (!p.by_row && lane == 0) p.join[gw] = entry;   // more rows than warps: teams are warps
 }
 
 // Joins the rows that lie in several ranges, 16 channels x 8 heads of one at a time.  WIDE: a CTA each, whose warps take
-// the pieces in turn and warp 0 merges the warps (rows of many pieces); else a warp each.
+// the pieces in turn; then warp w merges what all warps' lanes w hold.  Else a warp each.
 template <typename T, int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(kJoinWarps * 32) dense_join_kernel(const __grid_constant__ DenseParams p, int entries) {
-  constexpr int KS = D / 16;
-  __shared__ float4 so[WIDE ? kJoinWarps : 1][32], sml[WIDE ? kJoinWarps : 1][32];
+__global__ void __launch_bounds__((WIDE ? kJoinWarps : kNarrowWarps) * 32)
+    dense_join_kernel(const __grid_constant__ DenseParams p, int entries) {
+  constexpr int KS = D / 16, kAhead = 5;   // pieces requested at once
+  static_assert(!WIDE || kJoinWarps == 32, "a warp's lanes stand for the warps");
+  __shared__ float4 so[WIDE ? 32 : 1][33], sml[WIDE ? 32 : 1][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t item = WIDE ? blockIdx.x : (int64_t)blockIdx.x * kJoinWarps + warp;
-  const int at = (int)(item / (NT * KS)), nk = (int)(item - (int64_t)at * (NT * KS));
+  const int item = WIDE ? blockIdx.x : blockIdx.x * kNarrowWarps + warp;
+  const int at = item / (NT * KS), nk = item - at * (NT * KS);
   const int n = nk / KS, k = nk - n * KS;
   pdl_wait();
   pdl_trigger();
@@ -546,74 +589,106 @@ __global__ void __launch_bounds__(kJoinWarps * 32) dense_join_kernel(const __gri
   if (e.y < 2) return;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-  auto merge = [&](const float4& x, const float4& ml) {
-    const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.z);
-    const float a0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), a1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
-    const float w0 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - n0), w1 = ml.z == -INFINITY ? 0.f : exp2f(ml.z - n1);
-    o.x = o.x * a0 + x.x * w0;
-    o.y = o.y * a1 + x.y * w1;
-    o.z = o.z * a0 + x.z * w0;
-    o.w = o.w * a1 + x.w * w1;
-    l0 = l0 * a0 + ml.y * w0;
-    l1 = l1 * a1 + ml.w * w1;
-    m0 = n0;
-    m1 = n1;
-  };
-#pragma unroll 4
-  for (int i = WIDE ? warp : 0; i < e.y; i += WIDE ? kJoinWarps : 1) {
-    const size_t slot = 2 * (size_t)(e.z + i) + (i == 0 ? 1 : 0);
-    merge(p.o_part[(slot * NT * KS + nk) * 32 + lane], p.ml_part[slot * NT * 4 + n * 4 + (lane & 3)]);
+  auto weight = [](float m, float top) { return m == -INFINITY ? 0.f : exp2f(m - top); };
+  constexpr int kStep = WIDE ? kJoinWarps : 1;
+  for (int i0 = WIDE ? warp : 0; i0 < e.y; i0 += kStep * kAhead) {
+    float4 x[kAhead], ml[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * kStep;
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[u] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      if (i < e.y) {
+        const size_t slot = 2 * (size_t)(e.z + i) + (i == 0 ? 1 : 0);
+        x[u] = p.o_part[(slot * NT * KS + nk) * 32 + lane];
+        ml[u] = p.ml_part[slot * NT * 4 + n * 4 + (lane & 3)];
+      }
+    }
+    float t0 = m0, t1 = m1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      t0 = fmaxf(t0, ml[u].x);
+      t1 = fmaxf(t1, ml[u].z);
+    }
+    const float a0 = weight(m0, t0), a1 = weight(m1, t1);
+    o = make_float4(o.x * a0, o.y * a1, o.z * a0, o.w * a1);
+    l0 *= a0;
+    l1 *= a1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const float w0 = weight(ml[u].x, t0), w1 = weight(ml[u].z, t1);
+      o.x += x[u].x * w0;
+      o.y += x[u].y * w1;
+      o.z += x[u].z * w0;
+      o.w += x[u].w * w1;
+      l0 += ml[u].y * (ml[u].x == -INFINITY ? 1.f : w0);   // without weight it is 0, or NaN that has to stay
+      l1 += ml[u].w * (ml[u].z == -INFINITY ? 1.f : w1);
+    }
+    m0 = t0;
+    m1 = t1;
   }
+  const int b = e.x / p.Hkv, h = e.x - b * p.Hkv;
+  const size_t row0 = (size_t)b * p.Hq + (size_t)h * p.g;
   if constexpr (WIDE) {
     so[warp][lane] = o;
     sml[warp][lane] = make_float4(m0, l0, m1, l1);
     __syncthreads();
-    if (warp != 0) return;
-    const int used = min(kJoinWarps, e.y);
-    for (int w = 1; w < used; ++w) merge(so[w][lane], sml[w][lane]);
+    o = so[lane][warp];
+    const float4 ml = sml[lane][warp];
+    float top[2] = {ml.x, ml.z};
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+      top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
+      top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
+    }
+    const float w0 = weight(ml.x, top[0]), w1 = weight(ml.z, top[1]);
+    float v[6] = {o.x * w0, o.y * w1, o.z * w0, o.w * w1, ml.y * (ml.x == -INFINITY ? 1.f : w0),
+                  ml.w * (ml.z == -INFINITY ? 1.f : w1)};
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+#pragma unroll
+      for (int off = 16; off; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    const int head = n * 8 + 2 * (warp & 3);
+    if (lane == 0) finish<T, D>(p, row0, head, k, warp >> 2, make_float2(v[0], v[2]), top[0], v[4]);
+    if (lane == 1) finish<T, D>(p, row0, head + 1, k, warp >> 2, make_float2(v[1], v[3]), top[1], v[5]);
+  } else {
+    const int quad = lane >> 2, head = n * 8 + 2 * (lane & 3);
+    finish<T, D>(p, row0, head, k, quad, make_float2(o.x, o.z), m0, l0);
+    finish<T, D>(p, row0, head + 1, k, quad, make_float2(o.y, o.w), m1, l1);
   }
-  const int b = e.x / p.Hkv, h = e.x - b * p.Hkv, quad = lane >> 2, head = n * 8 + 2 * (lane & 3);
-  const size_t row0 = (size_t)b * p.Hq + (size_t)h * p.g;
-  finish<T, D>(p, row0, head, k, quad, make_float2(o.x, o.z), m0, l0);
-  finish<T, D>(p, row0, head + 1, k, quad, make_float2(o.y, o.w), m1, l1);
 }
 
-std::atomic<uint64_t> g_limit[16];
+std::atomic<uint64_t> g_limit[8];
 
-template <typename T, int D, int NT, bool TEAM>
-cudaError_t run(const DenseParams& p, int ctas, cudaStream_t s) {
-  constexpr int fixed = kWarps * kSlots * kSlotBytes + (TEAM ? kWarps * (D / 16) * 512 : 0);
-  constexpr int which = (std::is_same<T, __half>::value ? 8 : 0) + (D == 128 ? 4 : 0) + (NT - 1) * 2 + (TEAM ? 1 : 0);
-  cudaError_t e = ensure_smem_limit(dense_decode_kernel<T, D, NT, TEAM>, fixed + (2 * kMaxDecodeB + 1) * (int)sizeof(int),
+template <typename T, int D, int NT>
+cudaError_t run(DenseParams p, int ctas, cudaStream_t s) {
+  constexpr int fixed = kWarps * (kSlots * kSlotBytes + (D / 16) * 512);
+  constexpr int which = (std::is_same<T, __half>::value ? 4 : 0) + (D == 128 ? 2 : 0) + NT - 1;
+  cudaError_t e = ensure_smem_limit(dense_decode_kernel<T, D, NT>, fixed + (2 * kMaxDecodeB + 1) * (int)sizeof(int),
                                     g_limit[which]);
   if (e != cudaSuccess) return e;
+  const int rows = p.B * p.Hkv;
+  p.by_row = rows <= dense_ranges(ctas);
+  p.pad = rows < kTeamRows * ctas ? kPad : 0;
   const size_t smem = fixed + (2 * (size_t)p.B + 1) * sizeof(int);
-  e = launch_pdl(dense_decode_kernel<T, D, NT, TEAM>, dim3(ctas), dim3(kThreads), smem, s, p);
+  e = launch_pdl(dense_decode_kernel<T, D, NT>, dim3(ctas), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess) return e;
-  // a row has about ranges / rows + 1 pieces, at most; a warp takes up to nine
-  const int ranges = dense_ranges(ctas, p.B * p.Hkv), entries = p.by_row ? p.B * p.Hkv : ranges;
-  const int items = entries * NT * (D / 16);
-  if (ranges > 8 * entries)
+  const int entries = p.by_row ? rows : dense_ranges(ctas), items = entries * NT * (D / 16);
+  if (rows <= kWideRows)
     return launch_pdl(dense_join_kernel<T, D, NT, true>, dim3(items), dim3(kJoinWarps * 32), 0, s, p, entries);
-  return launch_pdl(dense_join_kernel<T, D, NT, false>, dim3((items + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, s,
-                    p, entries);
-}
-
-template <typename T, int D>
-cudaError_t run_width(const DenseParams& p, int ctas, cudaStream_t s) {
-  const bool team = dense_ranges(ctas, p.B * p.Hkv) == ctas;
-  if (p.g <= 8) return team ? run<T, D, 1, true>(p, ctas, s) : run<T, D, 1, false>(p, ctas, s);
-  return team ? run<T, D, 2, true>(p, ctas, s) : run<T, D, 2, false>(p, ctas, s);
+  return launch_pdl(dense_join_kernel<T, D, NT, false>, dim3((items + kNarrowWarps - 1) / kNarrowWarps),
+                    dim3(kNarrowWarps * 32), 0, s, p, entries);
 }
 
 template <typename T>
 cudaError_t run_type(const DenseParams& p, int D, int ctas, cudaStream_t s) {
-  return D == 64 ? run_width<T, 64>(p, ctas, s) : run_width<T, 128>(p, ctas, s);
+  if (D == 64) return p.g <= 8 ? run<T, 64, 1>(p, ctas, s) : run<T, 64, 2>(p, ctas, s);
+  return p.g <= 8 ? run<T, 128, 1>(p, ctas, s) : run<T, 128, 2>(p, ctas, s);
 }
 
 }  // namespace
 
-int dense_ranges(int ctas, int rows) { return rows >= kTeamRows * ctas ? ctas * kWarps : ctas; }
+int dense_ranges(int ctas) { return ctas * kWarps; }
 
 cudaError_t launch_dense_decode(const DenseParams& p, int D, int dtype, int ctas, cudaStream_t s) {
   return dtype == SEER_BF16 ? run_type<__nv_bfloat16>(p, D, ctas, s) : run_type<__half>(p, D, ctas, s);

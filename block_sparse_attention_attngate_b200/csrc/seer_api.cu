@@ -1224,7 +1224,7 @@ seer_status check_dense(const seer_dense_t* s) {
 
 // join entries | {m, l} of the pieces | outputs of the pieces (two pieces a range: its first and last sequence)
 size_t dense_layout(const seer_dense_t* s, int ctas, size_t* off_ml, size_t* off_o) {
-  const size_t ranges = seer::dense_ranges(ctas, s->batch * s->num_kv_heads);
+  const size_t ranges = seer::dense_ranges(ctas);
   const size_t tiles = s->num_q_heads / s->num_kv_heads > 8 ? 2 : 1;   // of eight heads
   *off_ml = up256(ranges * sizeof(int4));
   *off_o = *off_ml + up256(2 * ranges * tiles * 4 * sizeof(float4));
@@ -1262,8 +1262,8 @@ seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const se
   const bool paged = k->layout == SEER_KV_PAGED || v->layout == SEER_KV_PAGED;
   if (paged && shape->page_size < 1) return fail(SEER_ERR_INVALID_ARG, "page_size must be >= 1");
   const int64_t cap = std::min(kv_capacity(shape, k), kv_capacity(shape, v));
-  if (cap > INT32_MAX - 64 || cap / 32 + 1 >= ((int64_t)1 << 30) / shape->batch / shape->num_kv_heads)
-    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads * (cache capacity / 32 + 1) must be below 2^30");
+  if (cap > INT32_MAX - 64 || cap / 32 + 8 >= ((int64_t)1 << 30) / shape->batch / shape->num_kv_heads)
+    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads * (cache capacity / 32 + 8) must be below 2^30");
   int dev;
   DevFacts* df;
   if ((st = device_facts(&dev, &df)) != SEER_OK) return st;
@@ -1291,7 +1291,6 @@ seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const se
   p.join = reinterpret_cast<int4*>(ws);
   p.ml_part = reinterpret_cast<float4*>(ws + off_ml);
   p.o_part = reinterpret_cast<float4*>(ws + off_o);
-  p.by_row = p.B * p.Hkv <= seer::dense_ranges(df->sms, p.B * p.Hkv);
   p.err = err_word;
   cudaError_t e = seer::launch_dense_decode(p, shape->head_dim, shape->dtype, df->sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "dense_decode launch");

@@ -306,12 +306,13 @@ struct DenseParams {
   int4* join;                   // [entries] {row b * Hkv + h, pieces, first range, 0}; fewer than 2 pieces: nothing to join
   float4* ml_part;              // [2 * ranges][NT * 4] {m, l, m, l} of a lane's two heads (log2 domain)
   float4* o_part;               // [2 * ranges][NT * d / 16][32] register order
-  int32_t by_row;               // join entries are indexed by row, else by range
   int32_t* err;
+  int32_t by_row;               // join entries are indexed by row, else by range; set by the launch, as the next
+  int32_t pad;                  // units a row counts on top of its own
 };
 constexpr int kDenseMaxGroup = 16;
 constexpr int kDenseUnit = 32;  // tokens per scheduling unit
-int dense_ranges(int ctas, int rows);   // ranges of a launch over `rows` (sequence, KV head) rows, at most
+int dense_ranges(int ctas);     // ranges of a launch, at most
 cudaError_t launch_dense_decode(const DenseParams& p, int D, int dtype, int ctas, cudaStream_t s);
 
 // Record `msg` as the text seer_last_error() returns on this thread; returns `status`.
