@@ -48,8 +48,8 @@ constexpr int kMinUnits = 4;             // of a range, about
 constexpr int kSlotBytes = 4096;   // keys or values of one step
 constexpr int kMaskSteps = 4;      // steps whose masks are kept: more than are in the ring
 static_assert(kMaskSteps > (kSlots + 1) / 2, "a mask outlives its step");
-constexpr int kJoinWarps = 32, kNarrowWarps = 8;
-constexpr int kWideRows = 64;            // rows up to which a join takes a CTA for each
+constexpr int kJoinWarps = 16, kNarrowWarps = 8;
+constexpr int kWideRows = 8;             // rows up to which a join takes a CTA for each
 
 template <int D>
 constexpr int step_tokens() { return kSlotBytes / (2 * D); }   // 16 (d = 128) or 32 (d = 64)
@@ -159,7 +159,7 @@ __device__ __forceinline__ bool locate(const DenseParams& p, const KvPlain& kv, 
                                        int64_t* off) {
   if (kv.paged) {
     const bool ok = page_id >= 0 && page_id < kv.num_pages;
-    *off = ok ? page_id * kv.stride_b + h * kv.stride_h + (int64_t)(t % p.page) * kv.stride_t : 0;
+    *off = ok ? page_id * kv.stride_b + h * kv.stride_h + (int64_t)(t - p.by_page.div(t) * p.page) * kv.stride_t : 0;
     return ok;
   }
   *off = b * kv.stride_b + h * kv.stride_h + t * kv.stride_t;
@@ -269,17 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
   const int team = wide ? blockIdx.x : gw;
   const int G = min(wide ? gridDim.x : W, (axis + kMinUnits - 1) / kMinUnits);   // ranges
   int4 entry = make_int4(0, 0, 0, 0);
+  // ranges of base units, the first `extra` of them one more
+  const int base = G ? axis / G : 0, extra = axis - base * G;
   int u0 = 0, u1 = 0;
   Part rd, nx;     // being computed; of the next request (whose page ids are on their way)
   rd.t0 = rd.t1 = 0;
   if (team < G) {
-    if (axis < 1 << 20) {   // a 64-bit division takes its time
-      u0 = (int)((uint32_t)team * (uint32_t)axis / (uint32_t)G);
-      u1 = (int)((uint32_t)(team + 1) * (uint32_t)axis / (uint32_t)G);
-    } else {
-      u0 = (int)((int64_t)team * axis / G);
-      u1 = (int)((int64_t)(team + 1) * axis / G);
-    }
+    u0 = team * base + min(team, extra);
+    u1 = u0 + base + (team < extra ? 1 : 0);
     first_part(p, pre, len, u0, u1, &rd);
   }
   if (rd.t0 < rd.t1) {
@@ -300,8 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
       auto fetch_ids = [&]() {   // page ids of nx's tokens, one token a lane
         const int t = nx.t0 + nj * TS + lane;
         if (lane < TS && t < nx.t1) {
-          if (p.k.paged) id_k = p.k.block_table[(int64_t)nx.b * p.k.max_pages + t / p.page];
-          if (p.v.paged) id_v = p.v.block_table[(int64_t)nx.b * p.v.max_pages + t / p.page];
+          const int page = p.by_page.div(t);
+          if (p.k.paged) id_k = p.k.block_table[(int64_t)nx.b * p.k.max_pages + page];
+          if (p.v.paged) id_v = p.v.block_table[(int64_t)nx.b * p.v.max_pages + page];
         }
       };
       const int ch = lane % CPR;
@@ -559,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
         }
         if (head_in && lane == 0 && (!wide || warp == 0)) {
           // last range of the row: the one that holds its last unit
-          const int last = (int)(((int64_t)(rd.first + rd.units) * G - 1) / axis);
+          const int at = rd.first + rd.units - 1, big = extra * (base + 1);
+          const int last = whole ? team : (at < big ? at / (base + 1) : extra + (at - big) / base);
           const int4 e = make_int4(rd.b * p.Hkv + rd.h, last - team + 1, team, 0);
           if (p.by_row) p.join[e.x] = e;
           else if (!whole) entry = e;
@@ -571,13 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
 }
 
 // Joins the rows that lie in several ranges, 16 channels x 8 heads of one at a time.  WIDE: a CTA each, whose warps take
-// the pieces in turn; then warp w merges what all warps' lanes w hold.  Else a warp each.
+// the pieces in turn; then each warp merges two lanes of all of them.  Else a warp each.  (Co-resident joins, by smaller CTAs,
+// warp each.  Either leaves room beside a CTA of the kernel before, and so is there when that ends.
 template <typename T, int D, int NT, bool WIDE>
 __global__ void __launch_bounds__((WIDE ? kJoinWarps : kNarrowWarps) * 32)
     dense_join_kernel(const __grid_constant__ DenseParams p, int entries) {
   constexpr int KS = D / 16, kAhead = 5;   // pieces requested at once
-  static_assert(!WIDE || kJoinWarps == 32, "a warp's lanes stand for the warps");
-  __shared__ float4 so[WIDE ? 32 : 1][33], sml[WIDE ? 32 : 1][33];
+  __shared__ float4 so[WIDE ? kJoinWarps : 1][33], sml[WIDE ? kJoinWarps : 1][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = WIDE ? blockIdx.x : blockIdx.x * kNarrowWarps + warp;
   const int at = item / (NT * KS), nk = item - at * (NT * KS);
@@ -633,24 +632,29 @@ __global__ void __launch_bounds__((WIDE ? kJoinWarps : kNarrowWarps) * 32)
     so[warp][lane] = o;
     sml[warp][lane] = make_float4(m0, l0, m1, l1);
     __syncthreads();
-    o = so[lane][warp];
-    const float4 ml = sml[lane][warp];
-    float top[2] = {ml.x, ml.z};
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
-      top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
+    for (int col = warp; col < 32; col += kJoinWarps) {
+      const bool there = lane < kJoinWarps;
+      const float4 x = so[there ? lane : 0][col], ml = sml[there ? lane : 0][col];
+      float top[2] = {ml.x, ml.z};
+#pragma unroll
+      for (int off = 16; off; off >>= 1) {
+        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], off));
+        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], off));
+      }
+      const float w0 = weight(ml.x, top[0]), w1 = weight(ml.z, top[1]);
+      float v[6] = {x.x * w0, x.y * w1, x.z * w0, x.w * w1, ml.y * (ml.x == -INFINITY ? 1.f : w0),
+                    ml.w * (ml.z == -INFINITY ? 1.f : w1)};
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {
+        if (!there) v[i] = 0.f;
+#pragma unroll
+        for (int off = kJoinWarps / 2; off; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+      }
+      const int head = n * 8 + 2 * (col & 3);
+      if (lane == 0) finish<T, D>(p, row0, head, k, col >> 2, make_float2(v[0], v[2]), top[0], v[4]);
+      if (lane == 1) finish<T, D>(p, row0, head + 1, k, col >> 2, make_float2(v[1], v[3]), top[1], v[5]);
     }
-    const float w0 = weight(ml.x, top[0]), w1 = weight(ml.z, top[1]);
-    float v[6] = {o.x * w0, o.y * w1, o.z * w0, o.w * w1, ml.y * (ml.x == -INFINITY ? 1.f : w0),
-                  ml.w * (ml.z == -INFINITY ? 1.f : w1)};
-#pragma unroll
-    for (int i = 0; i < 6; ++i)
-#pragma unroll
-      for (int off = 16; off; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-    const int head = n * 8 + 2 * (warp & 3);
-    if (lane == 0) finish<T, D>(p, row0, head, k, warp >> 2, make_float2(v[0], v[2]), top[0], v[4]);
-    if (lane == 1) finish<T, D>(p, row0, head + 1, k, warp >> 2, make_float2(v[1], v[3]), top[1], v[5]);
   } else {
     const int quad = lane >> 2, head = n * 8 + 2 * (lane & 3);
     finish<T, D>(p, row0, head, k, quad, make_float2(o.x, o.z), m0, l0);

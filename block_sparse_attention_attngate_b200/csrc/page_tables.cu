@@ -99,7 +99,7 @@ __device__ __forceinline__ void warp_run(int n, int* lo, int* hi) {
 
 // x / page for 0 <= x < 2^31, and rounded up
 __device__ __forceinline__ int div(const PageParams& p, int x) {
-  return p.page == 1 ? x : (int)(__umulhi((uint32_t)x, p.magic) >> p.shift);
+  return p.by_page.div(x);
 }
 __device__ __forceinline__ int div_up(const PageParams& p, int x) {
   const int q = div(p, x);
@@ -298,23 +298,10 @@ __global__ void __launch_bounds__(THREADS) page_release_kernel(const PageParams 
 
 std::atomic<uint64_t> g_limit[2];
 
-// Multiplier and shift with floor(x / d) = mulhi(x, magic) >> shift for 0 <= x < 2^31 and 2 <= d < 2^31: with
-// s = ceil(log2 d) and magic = ceil(2^(31 + s) / d) < 2^32, the excess e = magic d - 2^(31 + s) is below d <= 2^s, so
-// x e < 2^(31 + s) and x magic / 2^(31 + s) stays below the next multiple of 1 / d.  mulhi takes 32 of the 31 + s bits.
-void set_divisor(PageParams& p) {
-  p.magic = 0;
-  p.shift = 0;
-  if (p.page < 2) return;
-  int s = 0;
-  while (((int64_t)1 << s) < p.page) ++s;
-  p.magic = (uint32_t)((((uint64_t)1 << (31 + s)) + p.page - 1) / p.page);
-  p.shift = s - 1;
-}
-
 // arrays: of p.B ints in shared memory; items: elements to write, at most
 cudaError_t launch(void (*small)(const PageParams), void (*large)(const PageParams), PageParams p, int arrays,
                    int64_t items, std::atomic<uint64_t>& done, cudaStream_t s) {
-  set_divisor(p);
+  p.by_page = divisor(p.page);
   p.in_place = p.seqlens == p.seqlens_out || p.free_count == p.free_count_out;
   const bool one = p.B <= kSmall * kPer && items <= 8 * kSmall;
   int ctas = 1;

@@ -1284,6 +1284,7 @@ seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const se
   p.g = shape->num_q_heads / shape->num_kv_heads;
   p.window = shape->window;
   p.page = paged ? shape->page_size : 1;
+  p.by_page = seer::divisor(p.page);
   p.cap = (int32_t)cap;
   const float scale = shape->softmax_scale > 0.f ? shape->softmax_scale : 1.0f / sqrtf((float)shape->head_dim);
   p.scale_log2 = scale * 1.4426950408889634f;

@@ -234,6 +234,24 @@ struct TruthParams {
 cudaError_t launch_gate_truth(const CUtensorMap& tk, const TruthParams& p, int D, int BLK, int sms, cudaStream_t s);
 int truth_chunk_blocks();
 
+// ---------------------------------------------------------------- division by a number known at the launch
+// x / d = mulhi(x, magic) >> shift for 0 <= x < 2^31 and d >= 2: with s = ceil(log2 d) and
+// magic = ceil(2^(31 + s) / d) < 2^32, the excess magic d - 2^(31 + s) is below d <= 2^s, so x times it is below
+// 2^(31 + s) and the quotient's floor is exact.  mulhi takes 32 of the 31 + s bits.
+struct Divisor {
+  int32_t d;
+  uint32_t magic;
+  int32_t shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int x) const { return d == 1 ? x : (int)(__umulhi((uint32_t)x, magic) >> shift); }
+#endif
+};
+inline Divisor divisor(int32_t d) {   // d >= 1
+  int s = 0;
+  while (((int64_t)1 << s) < d) ++s;
+  return {d, d < 2 ? 0u : (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), s - 1};
+}
+
 // ---------------------------------------------------------------- page tables
 struct PageParams {
   const int32_t* seqlens;       // [B]
@@ -249,8 +267,8 @@ struct PageParams {
   int32_t* positions;           // [max_tokens]
   int32_t B, page, num_pages, width, max_tokens;
   int32_t* err;
-  uint32_t magic;               // division by the page size; set by the launch, as the rest
-  int32_t shift, in_place;
+  Divisor by_page;              // set by the launch, as the next
+  int32_t in_place;
 };
 cudaError_t launch_page_plan(const PageParams& p, cudaStream_t s);
 cudaError_t launch_page_release(const PageParams& p, cudaStream_t s);
@@ -309,6 +327,7 @@ struct DenseParams {
   int32_t* err;
   int32_t by_row;               // join entries are indexed by row, else by range; set by the launch, as the next
   int32_t pad;                  // units a row counts on top of its own
+  Divisor by_page;
 };
 constexpr int kDenseMaxGroup = 16;
 constexpr int kDenseUnit = 32;  // tokens per scheduling unit
