@@ -8,7 +8,10 @@
 // and pieces (m_i, l_i, o_i) of one row join by the same rule.
 //
 // Bound: HBM -- every key and value is read once; 4 g flops a byte pair at most, a
-// tenth of what the warp-level tensor instructions sustain.
+// tenth of what the warp-level tensor instructions sustain (measured, graphs of the call, of the copy
+// bandwidth: 4 x 65536 tokens, 8 KV heads of 128, four query heads each, pages of 64, bf16: 170 us, 96 %; 16
+// sequences of 8000 to 32000 tokens, five heads, token-major pages of 16, fp16: 198 us, 101 %; 16 heads: 85 %; one sequence
+// of 2048 tokens, one KV head: 8.6 us, all of it latency: lengths, page ids, rows, the merge, the join's two round trips).
 //
 // Split.  The rows' (sequence, KV head) tokens in units of kDenseUnit are one long axis; equal ranges of it are the work
 // of as many teams, one wave.  A team's warps take its steps of 4 KB of keys and 4 KB of values in turn, each through a ring
@@ -17,8 +20,12 @@
 // size and stride: tokens that are out of range or on a bad page are filled
 // with zeros and masked, whatever lies there.
 // A team is a CTA when the rows are long (its warps merge their parts of a row in shared memory, so that a row leaves few
-// pieces), and a single warp when they are short (a merge costs more than the rows).  A row counts kPad units on top of its
-// own, about what a merge costs, so that ranges of many short rows beside few long ones take alike.
+// pieces: one row of 65536 tokens took 59 us with a piece from every warp, 15 us with one from every CTA), and a single warp
+// when they are short (a merge costs 1.5 us: 64 sequences of up to 600 tokens 64 us with CTAs, 24 us with warps).  A row
+// counts kPad units on top of its own, about what a merge costs, so that ranges of many short rows beside few long ones take
+// alike.
+// Twelve warps with three slots: the computation of a step is long (0.7 us), so its warps have to be many, and
+// more bytes in flight than the 96 KB an SM of this choice measured slower (12 x 4 slots: 185 us against 168, 8 x 6: 182).
 //
 // Products.  Both are taken transposed so that 16 tokens (or 16 channels) fill the
 // long side of the 16x8x16 instruction and the group's heads the short one (eight a
@@ -41,15 +48,15 @@ namespace {
 
 constexpr int kWarps = 12, kSlots = 3;   // of a CTA, of a warp's ring
 constexpr int kThreads = kWarps * 32;
-constexpr int kTeamRows = 6;             // rows an SM from which on teams are single warps whatever the lengths
-constexpr int kTeamUnits = 24;           // units of the mean row from which on teams are CTAs
+constexpr int kTeamRows = 6;       // rows an SM from which on teams are single warps whatever the lengths
+constexpr int kTeamUnits = 24;     // units of the mean row from which on teams are CTAs (1000 tokens: 22 us against 29)
 constexpr int kPad = 6;
-constexpr int kMinUnits = 4;             // of a range, about
+constexpr int kMinUnits = 4;       // of a range, about (64 short sequences: 24 us, 31 us with eight)
 constexpr int kSlotBytes = 4096;   // keys or values of one step
 constexpr int kMaskSteps = 4;      // steps whose masks are kept: more than are in the ring
 static_assert(kMaskSteps > (kSlots + 1) / 2, "a mask outlives its step");
-constexpr int kJoinWarps = 16, kNarrowWarps = 8;
-constexpr int kWideRows = 8;             // rows up to which a join takes a CTA for each
+constexpr int kJoinWarps = 32, kNarrowWarps = 8;
+constexpr int kWideRows = 8;       // rows up to which a join takes a CTA for each
 
 template <int D>
 constexpr int step_tokens() { return kSlotBytes / (2 * D); }   // 16 (d = 128) or 32 (d = 64)
@@ -280,88 +287,88 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
     first_part(p, pre, len, u0, u1, &rd);
   }
   if (rd.t0 < rd.t1) {
-      nx = rd;
-      int rj = wide ? warp : 0, nj = rj;   // this warp's next step of the part
-      bool nx_ok = true, values = false;   // the next request is of a step's keys, or of the values beside the last keys
-      auto settle = [&]() {   // to the part that holds step nj
-        while (nx_ok && nx.t0 + nj * TS >= nx.t1) {
-          nj -= (nx.t1 - nx.t0 + TS - 1) / TS;
-          nx_ok = next_part(p, pre, len, u0, u1, &nx);
-        }
-      };
-      settle();
-      int id_k = 0, id_v = 0, nstep = 0;
-      uint32_t fill = ring;                // slot of the next request
-      int64_t off_v = 0;                   // values of the last requested keys, one token a lane
-      uint32_t valid = 0;
-      auto fetch_ids = [&]() {   // page ids of nx's tokens, one token a lane
+    nx = rd;
+    int rj = wide ? warp : 0, nj = rj;   // this warp's next step of the part
+    bool nx_ok = true, values = false;   // the next request is of a step's keys, or of the values beside the last keys
+    auto settle = [&]() {   // to the part that holds step nj
+      while (nx_ok && nx.t0 + nj * TS >= nx.t1) {
+        nj -= (nx.t1 - nx.t0 + TS - 1) / TS;
+        nx_ok = next_part(p, pre, len, u0, u1, &nx);
+      }
+    };
+    settle();
+    int id_k = 0, id_v = 0, nstep = 0;
+    uint32_t fill = ring;                // slot of the next request
+    int64_t off_v = 0;                   // values of the last requested keys, one token a lane
+    uint32_t valid = 0;
+    auto fetch_ids = [&]() {   // page ids of nx's tokens, one token a lane
+      const int t = nx.t0 + nj * TS + lane;
+      if (lane < TS && t < nx.t1) {
+        const int page = p.by_page.div(t);
+        if (p.k.paged) id_k = p.k.block_table[(int64_t)nx.b * p.k.max_pages + page];
+        if (p.v.paged) id_v = p.v.block_table[(int64_t)nx.b * p.v.max_pages + page];
+      }
+    };
+    const int ch = lane % CPR;
+    auto copy = [&](const uint16_t* data, int64_t off) {
+#pragma unroll
+      for (int i = 0; i < TS / RPI; ++i) {
+        const int r = i * RPI + lane / CPR;
+        const int64_t a = __shfl_sync(0xffffffffu, off, r);
+        cp_async16<D>(fill + r * (2 * D) + ((ch ^ (r & 7)) << 4), data + a + ch * 8, (valid >> r) & 1);
+      }
+    };
+    auto request = [&]() {   // fill the next slot: a step's keys, then its values, in turn
+      if (values) {
+        copy(p.v.data, off_v);
+        values = false;
+      } else if (nx_ok) {
         const int t = nx.t0 + nj * TS + lane;
-        if (lane < TS && t < nx.t1) {
-          const int page = p.by_page.div(t);
-          if (p.k.paged) id_k = p.k.block_table[(int64_t)nx.b * p.k.max_pages + page];
-          if (p.v.paged) id_v = p.v.block_table[(int64_t)nx.b * p.v.max_pages + page];
+        int64_t off_k = 0;
+        off_v = 0;
+        bool good = lane < TS && t < nx.t1;
+        if (good) {
+          const bool gk = locate(p, p.k, id_k, nx.b, t, nx.h, &off_k);
+          const bool gv = locate(p, p.v, id_v, nx.b, t, nx.h, &off_v);
+          good = gk && gv;
+          if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
         }
-      };
-      const int ch = lane % CPR;
-      auto copy = [&](const uint16_t* data, int64_t off) {
+        valid = __ballot_sync(0xffffffffu, good);
+        if (lane == 0) masks[warp][nstep % kMaskSteps] = valid;
+        ++nstep;
+        copy(p.k.data, off_k);
+        values = true;
+        nj += S;
+        settle();
+        if (nx_ok) fetch_ids();
+      }
+      cp_commit();   // one group a slot, empty behind the range's end
+      fill = fill == ring + (kSlots - 1) * kSlotBytes ? ring : fill + kSlotBytes;
+    };
+    if (nx_ok) fetch_ids();
 #pragma unroll
-        for (int i = 0; i < TS / RPI; ++i) {
-          const int r = i * RPI + lane / CPR;
-          const int64_t a = __shfl_sync(0xffffffffu, off, r);
-          cp_async16<D>(fill + r * (2 * D) + ((ch ^ (r & 7)) << 4), data + a + ch * 8, (valid >> r) & 1);
-        }
-      };
-      auto request = [&]() {   // fill the next slot: a step's keys, then its values, in turn
-        if (values) {
-          copy(p.v.data, off_v);
-          values = false;
-        } else if (nx_ok) {
-          const int t = nx.t0 + nj * TS + lane;
-          int64_t off_k = 0;
-          off_v = 0;
-          bool good = lane < TS && t < nx.t1;
-          if (good) {
-            const bool gk = locate(p, p.k, id_k, nx.b, t, nx.h, &off_k);
-            const bool gv = locate(p, p.v, id_v, nx.b, t, nx.h, &off_v);
-            good = gk && gv;
-            if (!good) report(p.err, SEER_DEVERR_PAGE_INDEX);
-          }
-          valid = __ballot_sync(0xffffffffu, good);
-          if (lane == 0) masks[warp][nstep % kMaskSteps] = valid;
-          ++nstep;
-          copy(p.k.data, off_k);
-          values = true;
-          nj += S;
-          settle();
-          if (nx_ok) fetch_ids();
-        }
-        cp_commit();   // one group a slot, empty behind the range's end
-        fill = fill == ring + (kSlots - 1) * kSlotBytes ? ring : fill + kSlotBytes;
-      };
-      if (nx_ok) fetch_ids();
-#pragma unroll
-      for (int s = 0; s < kSlots - 1; ++s) request();
+    for (int s = 0; s < kSlots - 1; ++s) request();
 
-      uint32_t q[NT][KS][2];
-      float o[NT][KS][4], m[NT][2], l[NT][2];
-      int step = 0;
-      uint32_t take = ring;   // slot of the next keys or values to compute with
-      int parity = 0;
-      do {   // parts of the range
+    uint32_t q[NT][KS][2];
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+    int step = 0;
+    uint32_t take = ring;   // slot of the next keys or values to compute with
+    int parity = 0;
+    do {   // parts of the range
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int head = n * 8 + quad;
-          const uint16_t* src = p.q + ((size_t)rd.b * p.Hq + (size_t)rd.h * p.g + head) * D + c2;
+      for (int n = 0; n < NT; ++n) {
+        const int head = n * 8 + quad;
+        const uint16_t* src = p.q + ((size_t)rd.b * p.Hq + (size_t)rd.h * p.g + head) * D + c2;
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            q[n][k][0] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
-            q[n][k][1] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
-            o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
-          }
-          m[n][0] = m[n][1] = -INFINITY;
-          l[n][0] = l[n][1] = 0.f;
+        for (int k = 0; k < KS; ++k) {
+          q[n][k][0] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16) : 0u;
+          q[n][k][1] = head < p.g ? *reinterpret_cast<const uint32_t*>(src + k * 16 + 8) : 0u;
+          o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
-        for (; rd.t0 + rj * TS < rd.t1; rj += S) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+      }
+      for (; rd.t0 + rj * TS < rd.t1; rj += S) {
         // the next slot has arrived for every lane, and every lane is done with the one before, which is filled again
         auto next_slot = [&]() {
           cp_wait<kSlots - 2>();
@@ -463,115 +470,114 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
           }
 
         ++step;
-        }
-        rj -= (rd.t1 - rd.t0 + TS - 1) / TS;
+      }
+      rj -= (rd.t1 - rd.t0 + TS - 1) / TS;
 
-        // the range's part of the row is done
-        const bool head_in = rd.first >= u0, tail_in = rd.first + rd.units <= u1, whole = head_in && tail_in;
-        const size_t row0 = (size_t)rd.b * p.Hq + (size_t)rd.h * p.g;
-        const int slot = 2 * team + (head_in ? 1 : 0);
+      // the range's part of the row is done
+      const bool head_in = rd.first >= u0, tail_in = rd.first + rd.units <= u1, whole = head_in && tail_in;
+      const size_t row0 = (size_t)rd.b * p.Hq + (size_t)rd.h * p.g;
+      const int slot = 2 * team + (head_in ? 1 : 0);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 4);
+          l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
+          l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
+        }
+      if (wide) {
+        // The warps' parts: to the common maximum, then added up by all threads.  With two sets of maxima the next
+        // row's may be written while these are read; with one, the warps wait for the readers.
+        if (quad == 0)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            parts_ml[parity][warp][n * 8 + c2] = make_float2(m[n][0], l[n][0]);
+            parts_ml[parity][warp][n * 8 + c2 + 1] = make_float2(m[n][1], l[n][1]);
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          __syncthreads();   // the maxima are there (n = 0); the tile before has been added up
+          float f[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 4);
-            l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 8);
-            l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], 16);
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts_ml[parity][w][n * 8 + c2 + j].x);
+            f[j] = m[n][j] == -INFINITY ? 0.f : exp2f(m[n][j] - top);
           }
-        if (wide) {
-          // The warps' parts: to the common maximum, then added up by all threads.  With two sets of maxima the next
-          // row's may be written while these are read; with one, the warps wait for the readers.
-          if (quad == 0)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              parts_ml[parity][warp][n * 8 + c2] = make_float2(m[n][0], l[n][0]);
-              parts_ml[parity][warp][n * 8 + c2 + 1] = make_float2(m[n][1], l[n][1]);
+          for (int k = 0; k < KS; ++k)
+            parts_o[(warp * KS + k) * 32 + lane] =
+                make_float4(o[n][k][0] * f[0], o[n][k][1] * f[1], o[n][k][2] * f[0], o[n][k][3] * f[1]);
+          __syncthreads();
+          if (threadIdx.x < KS * 32) {
+            const int k = threadIdx.x >> 5;
+            float4 x = parts_o[threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+              const float4 y = parts_o[w * KS * 32 + threadIdx.x];
+              x.x += y.x;
+              x.y += y.y;
+              x.z += y.z;
+              x.w += y.w;
             }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            __syncthreads();   // the maxima are there (n = 0); the tile before has been added up
-            float f[2];
+            float mm[2], ll[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = -INFINITY;
+              mm[j] = -INFINITY;
+              ll[j] = 0.f;
 #pragma unroll
-              for (int w = 0; w < kWarps; ++w) top = fmaxf(top, parts_ml[parity][w][n * 8 + c2 + j].x);
-              f[j] = m[n][j] == -INFINITY ? 0.f : exp2f(m[n][j] - top);
+              for (int w = 0; w < kWarps; ++w) mm[j] = fmaxf(mm[j], parts_ml[parity][w][n * 8 + c2 + j].x);
+#pragma unroll
+              for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = parts_ml[parity][w][n * 8 + c2 + j];
+                ll[j] += ml.x == -INFINITY ? ml.y : ml.y * exp2f(ml.x - mm[j]);   // 0, or NaN kept
+              }
             }
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-              parts_o[(warp * KS + k) * 32 + lane] =
-                  make_float4(o[n][k][0] * f[0], o[n][k][1] * f[1], o[n][k][2] * f[0], o[n][k][3] * f[1]);
-            __syncthreads();
-            if (threadIdx.x < KS * 32) {
-              const int k = threadIdx.x >> 5;
-              float4 x = parts_o[threadIdx.x];
-#pragma unroll
-              for (int w = 1; w < kWarps; ++w) {
-                const float4 y = parts_o[w * KS * 32 + threadIdx.x];
-                x.x += y.x;
-                x.y += y.y;
-                x.z += y.z;
-                x.w += y.w;
-              }
-              float mm[2], ll[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                mm[j] = -INFINITY;
-                ll[j] = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mm[j] = fmaxf(mm[j], parts_ml[parity][w][n * 8 + c2 + j].x);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                  const float2 ml = parts_ml[parity][w][n * 8 + c2 + j];
-                  ll[j] += ml.x == -INFINITY ? ml.y : ml.y * exp2f(ml.x - mm[j]);   // 0, or NaN kept
-                }
-              }
-              if (whole) {
-                finish<T, D>(p, row0, n * 8 + c2, k, quad, make_float2(x.x, x.z), mm[0], ll[0]);
-                finish<T, D>(p, row0, n * 8 + c2 + 1, k, quad, make_float2(x.y, x.w), mm[1], ll[1]);
-              } else {
-                p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] = x;
-                if (k == 0 && quad == 0) p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(mm[0], ll[0], mm[1], ll[1]);
-              }
+            if (whole) {
+              finish<T, D>(p, row0, n * 8 + c2, k, quad, make_float2(x.x, x.z), mm[0], ll[0]);
+              finish<T, D>(p, row0, n * 8 + c2 + 1, k, quad, make_float2(x.y, x.w), mm[1], ll[1]);
+            } else {
+              p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] = x;
+              if (k == 0 && quad == 0) p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(mm[0], ll[0], mm[1], ll[1]);
             }
           }
-          if (kSets == 2) parity ^= 1;
-          else __syncthreads();
-        } else {
+        }
+        if (kSets == 2) parity ^= 1;
+        else __syncthreads();
+      } else {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              if (whole) {
-                finish<T, D>(p, row0, n * 8 + c2, k, quad, make_float2(o[n][k][0], o[n][k][2]), m[n][0], l[n][0]);
-                finish<T, D>(p, row0, n * 8 + c2 + 1, k, quad, make_float2(o[n][k][1], o[n][k][3]), m[n][1], l[n][1]);
-              } else {
-                p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] =
-                    make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
-              }
+          for (int k = 0; k < KS; ++k) {
+            if (whole) {
+              finish<T, D>(p, row0, n * 8 + c2, k, quad, make_float2(o[n][k][0], o[n][k][2]), m[n][0], l[n][0]);
+              finish<T, D>(p, row0, n * 8 + c2 + 1, k, quad, make_float2(o[n][k][1], o[n][k][3]), m[n][1], l[n][1]);
+            } else {
+              p.o_part[((size_t)slot * NT * KS + n * KS + k) * 32 + lane] =
+                  make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
             }
-            if (!whole && quad == 0)
-              p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(m[n][0], l[n][0], m[n][1], l[n][1]);
           }
+          if (!whole && quad == 0)
+            p.ml_part[(size_t)slot * NT * 4 + n * 4 + lane] = make_float4(m[n][0], l[n][0], m[n][1], l[n][1]);
         }
-        if (head_in && lane == 0 && (!wide || warp == 0)) {
-          // last range of the row: the one that holds its last unit
-          const int at = rd.first + rd.units - 1, big = extra * (base + 1);
-          const int last = whole ? team : (at < big ? at / (base + 1) : extra + (at - big) / base);
-          const int4 e = make_int4(rd.b * p.Hkv + rd.h, last - team + 1, team, 0);
-          if (p.by_row) p.join[e.x] = e;
-          else if (!whole) entry = e;
-        }
-      } while (next_part(p, pre, len, u0, u1, &rd));
-      cp_wait<0>();
+      }
+      if (head_in && lane == 0 && (!wide || warp == 0)) {
+        // last range of the row: the one that holds its last unit
+        const int at = rd.first + rd.units - 1, big = extra * (base + 1);
+        const int last = whole ? team : (at < big ? at / (base + 1) : extra + (at - big) / base);
+        const int4 e = make_int4(rd.b * p.Hkv + rd.h, last - team + 1, team, 0);
+        if (p.by_row) p.join[e.x] = e;
+        else if (!whole) entry = e;
+      }
+    } while (next_part(p, pre, len, u0, u1, &rd));
+    cp_wait<0>();
   }
   if (!p.by_row && lane == 0) p.join[gw] = entry;   // more rows than warps: teams are warps
 }
 
-// Joins the rows that lie in several ranges, 16 channels x 8 heads of one at a time.  WIDE: a CTA each, whose warps take
-// the pieces in turn; then each warp merges two lanes of all of them.  Else a warp each.  (Co-resident joins, by smaller CTAs,
-// warp each.  Either leaves room beside a CTA of the kernel before, and so is there when that ends.
+// Joins the rows that lie in several ranges, 16 channels x 8 heads of one at a time.  WIDE (few rows, so many pieces): a CTA
+// each, whose warps take the pieces in turn, before warp w merges what all warps' lanes w hold.  Else a warp each.
 template <typename T, int D, int NT, bool WIDE>
 __global__ void __launch_bounds__((WIDE ? kJoinWarps : kNarrowWarps) * 32)
     dense_join_kernel(const __grid_constant__ DenseParams p, int entries) {

@@ -1262,8 +1262,8 @@ seer_status seer_dense_decode(const seer_dense_t* shape, const void* q, const se
   const bool paged = k->layout == SEER_KV_PAGED || v->layout == SEER_KV_PAGED;
   if (paged && shape->page_size < 1) return fail(SEER_ERR_INVALID_ARG, "page_size must be >= 1");
   const int64_t cap = std::min(kv_capacity(shape, k), kv_capacity(shape, v));
-  if (cap > INT32_MAX - 64 || cap / 32 + 8 >= ((int64_t)1 << 30) / shape->batch / shape->num_kv_heads)
-    return fail(SEER_ERR_UNSUPPORTED, "batch * num_kv_heads * (cache capacity / 32 + 8) must be below 2^30");
+  if (cap >= (int64_t)1 << 30 || cap / 32 + 8 >= ((int64_t)1 << 30) / shape->batch / shape->num_kv_heads)
+    return fail(SEER_ERR_UNSUPPORTED, "cache capacity and batch * num_kv_heads * (capacity / 32 + 8) must be below 2^30");
   int dev;
   DevFacts* df;
   if ((st = device_facts(&dev, &df)) != SEER_OK) return st;

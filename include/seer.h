@@ -607,7 +607,7 @@ typedef struct {
  *   seqlens    device int32 [B], L_b counting the new token
  *   workspace  device, >= seer_dense_decode_workspace_bytes(shape) bytes, 16-byte aligned, no initial
  *              value needed; calls on one workspace must not overlap on the GPU
- * batch <= 4096, batch * Hkv < 2^24 and batch * Hkv * (cache capacity / 32 + 8) < 2^30.  Two launches:
+ * batch <= 4096, batch * Hkv < 2^24, capacity < 2^30 and batch * Hkv * (capacity / 32 + 8) < 2^30.  Two launches:
  * the split pass, one wave over equal ranges of all rows' tokens, and the join of the rows that lie in
  * several ranges.  Results do not depend on timing (no atomics).
  */

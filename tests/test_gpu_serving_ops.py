@@ -482,6 +482,25 @@ def test_dense_many_rows_and_batches():
     check_dense(5, 2, 2, 64, [0] * 5, 8, 8, BF16, "head")
 
 
+@pytest.mark.parametrize("g", [1, 5, 8, 9, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_dense_long_rows(g, d):
+    """Rows long enough to be split over CTAs whose warps merge."""
+    check_dense(3, g, 2, d, [3000, 1, 2111], 3000, 48, BF16, "head", seed=g)
+    check_dense(2, g, 1, d, [20001, 0], 20001, 16, FP16, "token", seed=g)
+    check_dense(1, g, 3, d, [6007], 6100, 64, BF16, "flat", window=4999, seed=g)
+
+
+def test_dense_mixed_lengths():
+    """Few long rows beside many short ones, in both orders, and rows that leave many pieces."""
+    r = random.Random(8)
+    short = [r.randint(0, 40) for _ in range(45)]
+    check_dense(47, 4, 2, 128, [9000] + short + [7000], 9000, 64, BF16, "head")
+    check_dense(47, 4, 2, 64, short + [30000, 1], 30000, 256, BF16, "flat")
+    check_dense(90, 2, 4, 64, short * 2, 40, 8, FP16, "token")
+    check_dense(12, 8, 1, 128, [5000 + 37 * i for i in range(12)], 6000, 16, BF16, "token")
+
+
 def test_dense_scales_and_peaks():
     check_dense(2, 4, 2, 128, [700, 300], 700, 64, BF16, "head", scale=0.5)
     check_dense(2, 4, 2, 128, [700, 300], 700, 64, FP16, "head", q_scale=12.0)    # near one-hot weights
