@@ -130,19 +130,24 @@ __device__ __forceinline__ void clip(const DenseParams& p, const int* len, int u
   r->t1 = left >= r->units ? hi : lo + left * kDenseUnit;
 }
 
-// The part of the row that unit u0 < Hkv * pre[B] belongs to; empty when the range ends in the row's padding.
+// The part of the row that unit u0 < Hkv * pre[B] belongs to; empty when the range ends in the row's padding.  For whole warps.
 __device__ __forceinline__ void first_part(const DenseParams& p, const int* pre, const int* len, int u0, int u1, Part* r) {
   // the last sequence that starts at or before u0 (a sequence without units shares its successor's start)
   int b = 0;
-  for (int hi = p.B; hi - b > 1;) {
-    const int mid = (b + hi) >> 1;
-    if (pre[mid] * p.Hkv <= u0) b = mid;
-    else hi = mid;
+  if (p.B <= 32) {
+    const int lane = threadIdx.x & 31;
+    b = __popc(__ballot_sync(0xffffffffu, lane < p.B && pre[min(lane, p.B)] * p.Hkv <= u0)) - 1;
+  } else {
+    for (int hi = p.B; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (pre[mid] * p.Hkv <= u0) b = mid;
+      else hi = mid;
+    }
   }
   const int span = pre[b + 1] - pre[b];
   r->b = b;
   r->units = span - p.pad;
-  r->h = (u0 - pre[b] * p.Hkv) / span;
+  r->h = (int)((uint32_t)(u0 - pre[b] * p.Hkv) / (uint32_t)span);
   r->first = pre[b] * p.Hkv + r->h * span + p.pad;
   clip(p, len, u0, u1, r);
 }
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
   const int G = min(wide ? gridDim.x : W, (axis + kMinUnits - 1) / kMinUnits);   // ranges
   int4 entry = make_int4(0, 0, 0, 0);
   // ranges of base units, the first `extra` of them one more
-  const int base = G ? axis / G : 0, extra = axis - base * G;
+  const int base = G ? (int)((uint32_t)axis / (uint32_t)G) : 0, extra = axis - base * G;
   int u0 = 0, u1 = 0;
   Part rd, nx;     // being computed; of the next request (whose page ids are on their way)
   rd.t0 = rd.t1 = 0;

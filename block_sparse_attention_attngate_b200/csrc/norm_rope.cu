@@ -286,12 +286,13 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas) norm_rope_kernel(const
         unpack(x0[u], a);
         unpack(x1[u], b);
         if (kd.weight) {
-          F2 q = mul2(a[0], a[0]);
+          F2 qa = mul2(a[0], a[0]), qb = mul2(b[0], b[0]);
 #pragma unroll
-          for (int e = 1; e < 4; ++e) q = fma2(a[e], a[e], q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q = fma2(b[e], b[e], q);
-          const float2 qs = split(q);
+          for (int e = 1; e < 4; ++e) {
+            qa = fma2(a[e], a[e], qa);
+            qb = fma2(b[e], b[e], qb);
+          }
+          const float2 qs = split(add2(qa, qb));
           const float rs = rsqrtf(row_sum<LPR>(qs.x + qs.y) * (1.0f / D) + p.eps);
           const F2 r2 = f2(rs, rs);
           F2 wa[4], wb[4];
@@ -463,37 +464,36 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
           }
         }
         if (kd.weight) {
-          F2 ga[4], gb[4], xa[4], xb[4];
+          F2 wa[4], wb[4], xa[4], xb[4], ga[4], gb[4];   // ga: dy x
           unpack(x0, xa);
           unpack(x1, xb);
-          unpack(w0, ga);
-          unpack(w1, gb);
-          F2 q = mul2(xa[0], xa[0]);
+          unpack(w0, wa);
+          unpack(w1, wb);
+          F2 qa = mul2(xa[0], xa[0]), qb = mul2(xb[0], xb[0]);
+          ga[0] = mul2(a[0], xa[0]);
+          gb[0] = mul2(b[0], xb[0]);
+          F2 da = mul2(ga[0], wa[0]), db = mul2(gb[0], wb[0]);
 #pragma unroll
-          for (int e = 1; e < 4; ++e) q = fma2(xa[e], xa[e], q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            q = fma2(xb[e], xb[e], q);
-            ga[e] = mul2(a[e], ga[e]);
-            gb[e] = mul2(b[e], gb[e]);
+          for (int e = 1; e < 4; ++e) {
+            qa = fma2(xa[e], xa[e], qa);
+            qb = fma2(xb[e], xb[e], qb);
+            ga[e] = mul2(a[e], xa[e]);
+            gb[e] = mul2(b[e], xb[e]);
+            da = fma2(ga[e], wa[e], da);
+            db = fma2(gb[e], wb[e], db);
           }
-          F2 d = mul2(xa[0], ga[0]);
-#pragma unroll
-          for (int e = 1; e < 4; ++e) d = fma2(xa[e], ga[e], d);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d = fma2(xb[e], gb[e], d);
-          const float2 qs = split(q), ds = split(d);
+          const float2 qs = split(add2(qa, qb)), ds = split(add2(da, db));
           const float rs = rsqrtf(row_sum<LPR>(qs.x + qs.y) * (1.0f / D) + p.eps);
           const float k = row_sum<LPR>(ds.x + ds.y) * (-1.0f / D) * rs * rs;
           const F2 r2 = f2(rs, rs), k2 = f2(k, k);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (mine) {
-              dw0[e] = fma2(a[e], mul2(xa[e], r2), dw0[e]);
-              dw1[e] = fma2(b[e], mul2(xb[e], r2), dw1[e]);
+              dw0[e] = fma2(ga[e], r2, dw0[e]);
+              dw1[e] = fma2(gb[e], r2, dw1[e]);
             }
-            a[e] = mul2(r2, fma2(xa[e], k2, ga[e]));
-            b[e] = mul2(r2, fma2(xb[e], k2, gb[e]));
+            a[e] = mul2(r2, fma2(xa[e], k2, mul2(a[e], wa[e])));
+            b[e] = mul2(r2, fma2(xb[e], k2, mul2(b[e], wb[e])));
           }
         }
         if (mine) {

@@ -302,7 +302,7 @@ std::atomic<uint64_t> g_limit[2];
 cudaError_t launch(void (*small)(const PageParams), void (*large)(const PageParams), PageParams p, int arrays,
                    int64_t items, std::atomic<uint64_t>& done, cudaStream_t s) {
   p.by_page = divisor(p.page);
-  p.in_place = p.seqlens == p.seqlens_out || p.free_count == p.free_count_out;
+  p.in_place = p.seqlens == p.seqlens_out || p.free_count == p.free_count_out || p.per_request == p.seqlens_out;
   const bool one = p.B <= kSmall * kPer && items <= 8 * kSmall;
   int ctas = 1;
   if (!one && items > 4 * kLarge)

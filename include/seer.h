@@ -602,6 +602,7 @@ typedef struct {
  * L_b and before the window are not used (they may hold anything, NaN included).
  *
  *   q, out     device [B, Hq, d] of the shape's type;  lse_out device fp32 [B, Hq] or NULL
+ *   q, out     may be the same memory
  *   k, v       caches (see seer_kv_t) of the shape's type, contiguous or paged with page_size tokens per
  *              page (the two may differ in layout and table)
  *   seqlens    device int32 [B], L_b counting the new token

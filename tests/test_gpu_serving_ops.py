@@ -517,6 +517,45 @@ def test_dense_bad_pages_and_lengths():
     check_dense(3, 4, 2, 64, [49, -7, 2 ** 31 - 1], 48, 16, BF16, "head", err_bits=pkg.DEVERR_COUNT)
 
 
+def test_dense_keys_and_values_of_different_layouts():
+    """Keys paged and values contiguous, and the two paged by different tables; the output on the query's memory."""
+    pkg, B, g, H, d, page, cap = S(), 3, 4, 2, 128, 24, 900
+    gn = gen(21)
+    a, b, c = (Rows(gn, B, H, cap, d, page, BF16, o) for o in ("head", "token", "flat"))
+    lens = [900, 31, 470]
+    for k, v in ((a, c), (c, b), (a, b)):
+        q = rnd(gn, B, g * H, d, dt=BF16)
+        out, lse = torch.empty_like(q), torch.empty(B, g * H, device="cuda")
+        ws = pkg.alloc_dense_workspace(B, g * H, H, d)
+        pkg.dense_decode(q, k.kc, v.vc, i32(lens), out, ws, lse=lse)
+
+        def rows(i, h):
+            K, V = k(i, h)[0][:cap], v(i, h)[1][:cap]
+            return K, V, torch.ones(cap, dtype=torch.bool, device="cuda")
+
+        rows.heads = H
+        o, l, bo, bl = R.dense(q, rows, lens, 0, d ** -0.5, BF16)
+        R.close(out, o, bo)
+        assert ((lse.double() - l).abs() <= bl).all()
+        pkg.dense_decode(q, k.kc, v.vc, i32(lens), q, ws)
+        assert torch.equal(q, out)
+
+
+def test_dense_nan_stays_in_its_row():
+    """A NaN key or value that is seen shows in its sequence's rows of that head alone."""
+    pkg, B, g, H, d = S(), 2, 4, 2, 64
+    for T in (60, 2500):
+        gn = gen(T)
+        rows = Rows(gn, B, H, T, d, 64, BF16, "flat")
+        rows.k[0, 1, T // 2] = math.nan
+        q = rnd(gn, B, g * H, d, dt=BF16)
+        out, lse = torch.empty_like(q), torch.empty(B, g * H, device="cuda")
+        pkg.dense_decode(q, rows.kc, rows.vc, i32([T, T]), out, pkg.alloc_dense_workspace(B, g * H, H, d), lse=lse)
+        bad = torch.zeros(B, g * H, dtype=torch.bool, device="cuda")
+        bad[0, g:] = True
+        assert torch.equal(out.isnan().all(-1), bad) and torch.equal(out.isnan().any(-1), bad) and torch.equal(lse.isnan(), bad)
+
+
 def test_dense_offsets_past_32_bits():
     """A contiguous cache whose second sequence starts beyond 2^32 bytes and 2^31 elements."""
     pkg, d, T = S(), 128, 130
