@@ -49,9 +49,10 @@ namespace {
 constexpr int kWarps = 12, kSlots = 3;   // of a CTA, of a warp's ring
 constexpr int kThreads = kWarps * 32;
 constexpr int kTeamRows = 6;       // rows an SM from which on teams are single warps whatever the lengths
-constexpr int kTeamUnits = 24;     // units of the mean row from which on teams are CTAs (1000 tokens: 22 us against 29)
+constexpr int kTeamUnits = 24;     // units of the mean token's row from which on teams are CTAs (1000 tokens: 22 us against 29)
 constexpr int kPad = 6;
-constexpr int kMinUnits = 4;       // of a range, about (64 short sequences: 24 us, 31 us with eight)
+constexpr int kMinUnits = 4, kMinUnitsTeam = 8;   // of a range, about (warps: 64 short sequences 24 us, 31 us with eight)
+constexpr int kWholeUnits = 24;    // rows up to this, padding included, are not split: a join takes 2.4 us (100 tokens: 6.5 us against 8.8)
 constexpr int kSlotBytes = 4096;   // keys or values of one step
 constexpr int kMaskSteps = 4;      // steps whose masks are kept: more than are in the ring
 static_assert(kMaskSteps > (kSlots + 1) / 2, "a mask outlives its step");
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t masks[kWarps][kMaskSteps];
   __shared__ int scan_ws[kWarps];
+  __shared__ float squares_ws[kWarps];
   constexpr int kSets = NT == 1 ? 2 : 1;   // shared memory is full with two of 16 heads
   __shared__ float2 parts_ml[kSets][kWarps][NT * 8];   // the warps' maxima and sums
   constexpr int kRing = kWarps * kSlots * kSlotBytes, kParts = kWarps * KS * 512;
@@ -213,11 +215,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
 
   // exclusive scan of the sequences' units, a row's padding with them
   int total = 0, filled = 0;   // units of one KV head's rows, rows with tokens
+  float sq = 0.f;              // squares of the rows' own units
   auto row_units = [&](int b, int* L) {
     *L = b < p.B ? p.seqlens[b] : 0;
     if (*L > p.cap && blockIdx.x == 0) report(p.err, SEER_DEVERR_COUNT);
     const int n = units_of(p, *L);
     return n > 0 ? n + p.pad : 0;
+  };
+  auto squares = [&](int n) {
+    float x = n > 0 ? (float)(n - p.pad) : 0.f;
+    x *= x;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
   };
   auto warp_scan = [&](int x) {   // inclusive
 #pragma unroll
@@ -236,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
     }
     total = __shfl_sync(0xffffffffu, inc, 31);
     filled = __popc(__ballot_sync(0xffffffffu, n > 0));
+    sq = squares(n);
     if (lane == 0) pre[p.B] = total;
     __syncwarp();
   } else {
@@ -243,13 +254,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
       const int b = b0 + threadIdx.x;
       int L;
       const int n = row_units(b, &L), inc = warp_scan(n);
-      if (lane == 31) scan_ws[warp] = inc;
+      const float x = squares(n);
+      if (lane == 31) {
+        scan_ws[warp] = inc;
+        squares_ws[warp] = x;
+      }
       filled += __syncthreads_count(n > 0);
       int before = 0, all = 0;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         before += w < warp ? scan_ws[w] : 0;
         all += scan_ws[w];
+        sq += squares_ws[w];
       }
       if (b < p.B) {
         pre[b] = total + before + inc - n;
@@ -264,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
 
   const int W = gridDim.x * kWarps, gw = blockIdx.x * kWarps + warp;
   const int axis = total * p.Hkv;   // units of all rows
-  const bool wide = p.pad > 0 && total >= filled * (kTeamUnits + kPad);
+  // CTAs when every row can have one, or when the mean token's row is long
+  const bool wide = p.pad > 0 && (filled * p.Hkv <= (int)gridDim.x || sq >= (float)kTeamUnits * (total - filled * p.pad));
   const int S = wide ? kWarps : 1;  // warps of a team
   // rows without a token
   for (int r = gw; r < p.B * p.Hkv; r += W) {
@@ -279,7 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
 
   const uint32_t ring = smem_u32(smem) + warp * kSlots * kSlotBytes;
   const int team = wide ? blockIdx.x : gw;
-  const int G = min(wide ? gridDim.x : W, (axis + kMinUnits - 1) / kMinUnits);   // ranges
+  const int rows = filled * p.Hkv;
+  int G = (axis + (wide ? kMinUnitsTeam : kMinUnits) - 1) / (wide ? kMinUnitsTeam : kMinUnits);   // ranges
+  if (wide) G = axis <= kWholeUnits * rows ? rows : max(G, rows);
+  G = min(G, wide ? (int)gridDim.x : W);
   int4 entry = make_int4(0, 0, 0, 0);
   // ranges of base units, the first `extra` of them one more
   const int base = G ? (int)((uint32_t)axis / (uint32_t)G) : 0, extra = axis - base * G;
