@@ -11,7 +11,7 @@
 // tenth of what the warp-level tensor instructions sustain (measured, graphs of the call, of the copy
 // bandwidth: 4 x 65536 tokens, 8 KV heads of 128, four query heads each, pages of 64, bf16: 170 us, 96 %; 16
 // sequences of 8000 to 32000 tokens, five heads, token-major pages of 16, fp16: 198 us, 101 %; 16 heads: 85 %; one sequence
-// of 2048 tokens, one KV head: 8.6 us, all of it latency: lengths, page ids, rows, the merge, the join's two round trips).
+// of 2048 tokens, one KV head: 8.5 us, all of it latency: lengths, page ids, rows, the merge, the join's two round trips).
 //
 // Split.  The rows' (sequence, KV head) tokens in units of kDenseUnit are one long axis; equal ranges of it are the work
 // of as many teams, one wave.  A team's warps take its steps of 4 KB of keys and 4 KB of values in turn, each through a ring

@@ -11,7 +11,7 @@
 //
 // Bound: HBM -- every input is read once and every output written once.  Measured (graphs of the call, against the
 // copy bandwidth): 8192 tokens of 32 + 8 heads of 128, rotated and plain outputs and both caches in bf16, 51 us, 86 %
-// (the time does not move with the batch, the unit or the CTAs an SM); the gradients of the same rows 49 us, 79 %; 2049
+// (the time does not move with the batch, the unit or the CTAs an SM); the gradients of the same rows 48 us, 80 %; 2049
 // tokens of 40 + 8 heads, half rotated, 11 us, 71 %.  The arithmetic is close behind the memory in the last two, so
 // it is done two channels at a time (f32x2 instructions: 53 us against 50 without) and addresses are stepped.
 //
@@ -26,9 +26,11 @@
 // A pass is 32 / (D / 16) heads of one token.  Warps are independent.  A token's angles (fp64 products, whole
 // turns taken off) are computed by the warp's lanes while the token's first rows are on their way, exchanged
 // through the warp's own shared memory and kept in registers for all its heads.
-// A warp takes up to kUnitPasses passes and ends; a unit's first rows, position, slot and the live count are
-// all requested at once.  (Staying CTAs with equal shares measured 10-20 % slower in both directions: some SMs
-// get less of the memory's bandwidth than others, and the rest wait for them at the end.)
+// Forward, a warp takes up to kUnitPasses passes of one token and ends; its first rows, position, slot and the live count are
+// all requested at once.  Backward, it takes kRunPasses passes of the list of all tokens' passes, and keeps
+// some in flight through a ring in shared memory (cp.async; every lane reads back what it has requested itself, so no
+// lane waits for another).  (Staying CTAs with equal shares measured 10-20 % slower in both directions: some SMs get less
+// of the memory's bandwidth than others, and the rest wait for them at the end.)
 #include "seer_device.cuh"
 #include "seer_internal.h"
 
@@ -529,17 +531,21 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_ke
 }
 
 // Sums of the CTAs' partial weight gradients in a fixed order: eight channels of one kind a CTA, 128 threads each.
+struct WeightSums {
+  const float* partial;
+  float* dw[2];   // null: absent
+  int cta0[2], ctas[2];
+};
 template <int D>
-__global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant__ WeightSums p) {
   __shared__ float red[32][8];
   const int k = blockIdx.x / (D / 8), c = blockIdx.x % (D / 8) * 8 + (threadIdx.x & 7), g = threadIdx.x >> 3;
-  const NormKind& kd = p.kind[k];
   pdl_wait();
   pdl_trigger();
-  if (!kd.dw) return;
+  if (!p.dw[k]) return;
   float s = 0.f;
 #pragma unroll 8
-  for (int i = g; i < kd.ctas; i += 128) s += p.partial[(size_t)(kd.cta0 + i) * D + c];
+  for (int i = g; i < p.ctas[k]; i += 128) s += p.partial[(size_t)(p.cta0[k] + i) * D + c];
   s += __shfl_xor_sync(0xffffffffu, s, 8);
   s += __shfl_xor_sync(0xffffffffu, s, 16);
   if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][threadIdx.x & 7] = s;
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const __grid_constant
   if (threadIdx.x < 8) {
 #pragma unroll
     for (int w = 1; w < 32; ++w) s += red[w][threadIdx.x];
-    kd.dw[c] = s;
+    p.dw[k][c] = s;
   }
 }
 
@@ -600,7 +606,13 @@ cudaError_t backward_of(NormParams p, int sms, cudaStream_t s) {
   }
   e = launch_pdl(norm_rope_backward_kernel<T, D, Y>, dim3(grid), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess || !(p.kind[0].dw || p.kind[1].dw)) return e;
-  return launch_pdl(norm_weight_kernel<D>, dim3(2 * (D / 8)), dim3(1024), 0, s, p);
+  WeightSums w = {p.partial};
+  for (int k = 0; k < 2; ++k) {
+    w.dw[k] = p.kind[k].dw;
+    w.cta0[k] = p.kind[k].cta0;
+    w.ctas[k] = p.kind[k].ctas;
+  }
+  return launch_pdl(norm_weight_kernel<D>, dim3(2 * (D / 8)), dim3(1024), 0, s, w);
 }
 
 template <typename T, int D>
