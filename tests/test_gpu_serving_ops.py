@@ -747,3 +747,129 @@ def test_refusals_on_the_device():
         pkg.dense_decode(q, kv, kv, lens.float(), torch.empty_like(q), ws)
     with pytest.raises(TypeError):
         pkg.dense_decode(q.half(), kv, kv, lens, q.half(), ws)
+
+
+def test_norm_rope_offsets_past_32_bits():
+    """Rows 2^31 elements apart, read and written."""
+    T, d = 2, 64
+    gn = gen(4)
+    base = torch.zeros((1 << 31) + 4096, dtype=BF16, device="cuda")
+    far = base.as_strided((T, 1, d), (1 << 31, d, 1))
+    x, w, pos = rnd(gn, T, 1, d, dt=BF16), rnd(gn, d, dt=BF16), i32([3, 70000])
+    want, dwant, gw, gw2 = torch.empty_like(x), torch.empty_like(x), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    S().qk_norm_rope(x, None, pos, want, q_weight=w)
+    far.copy_(x)
+    S().qk_norm_rope(far, None, pos, far, q_weight=w)
+    assert torch.equal(far, want)
+    ws = S().alloc_norm_workspace(d)
+    S().qk_norm_rope_backward(want, None, x, None, pos, dwant, None, ws, w, None, gw, None)
+    S().qk_norm_rope_backward(far, None, x, None, pos, far, None, ws, w, None, gw2, None)
+    assert torch.equal(far, dwant) and torch.equal(gw, gw2)
+
+
+def test_norm_rope_backward_of_many_rows():
+    """More passes than the workspace has rows for at the usual run (every warp then takes more of them)."""
+    T, Hq, Hkv, d, rope = 20011, 64, 8, 64, 64
+    g, q, k, v, wq, wk, pos = rope_problem(1, T, Hq, Hkv, d, BF16)
+    gq, gk = rnd(g, T, Hq, d, dt=BF16), rnd(g, T, Hkv, d, dt=BF16)
+    dq, dk, dwq, dwk = torch.empty_like(gq), torch.empty_like(gk), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    S().qk_norm_rope_backward(gq, gk, q, k, pos, dq, dk, S().alloc_norm_workspace(d), wq, wk, dwq, dwk)
+    for x, w, z, dx, dw in ((q, wq, gq, dq, dwq), (k, wk, gk, dk, dwk)):
+        sums, sizes = 0, 0
+        for a in range(0, T, 5000):
+            c = slice(a, a + 5000)
+            rx, rw, bx, mw = R.norm_grad(x[c], w, 1e-6, pos[c], 1e6, rope, z[c], None)
+            R.close(dx[c], rx, bx, "dx")
+            sums, sizes = sums + rw, sizes + mw
+        # a lane adds at most 8 x 11 rows, the CTA's 32 lanes of a channel and the CTAs (at most 4096) follow
+        R.close(dw, sums, (2.0 ** -17 + (88 + 32 + 4096 / 128 + 40) * R.F) * sizes, "dw")
+
+
+def test_serving_step_in_a_graph():
+    """A decode step -- pages, norm + rotation + cache write, dense attention -- captured once, replayed with lengths and the
+    free count carried on in place, against the same calls made one by one on a side stream."""
+    pkg, B, Hq, H, d, page, width, dt = S(), 5, 8, 2, 64, 16, 8, FP16
+    gn = gen(31)
+    pages, steps, wq, wk = B * width, 6, rnd(gn, d, dt=dt), rnd(gn, d, dt=dt)
+    xs = [rnd(gn, B, Hq + 2 * H, d, dt=dt) for _ in range(steps)]
+    order, lens0 = torch.randperm(pages, generator=gn, device="cuda").int(), [0, 15, 16, 31, 40]
+
+    class State:
+        def __init__(self):
+            held = [-(-n // page) for n in lens0]
+            ids, at, table = order.tolist(), 0, [[-1] * width for _ in range(B)]
+            for b, n in enumerate(held):
+                table[b][:n] = ids[at:at + n]
+                at += n
+            self.L, self.T, self.F, self.C = i32(lens0), i32(table), i32(ids[at:] + [-1] * at), i32([pages - at])
+            self.cu, self.slots, self.pos, self.err, self.one = i32([0] * (B + 1)), i32([0] * B), i32([0] * B), i32([0]), i32([1] * B)
+            g2 = gen(32)
+            self.kc, self.vc = rnd(g2, pages, H, page, d, dt=dt), rnd(g2, pages, H, page, d, dt=dt)
+            self.K, self.V = pkg.KVCache.paged(self.kc, self.T), pkg.KVCache.paged(self.vc, self.T)
+            self.x, self.q = torch.zeros(B, Hq + 2 * H, d, dtype=dt, device="cuda"), torch.zeros(B, Hq, d, dtype=dt, device="cuda")
+            self.out, self.lse = torch.zeros_like(self.q), torch.zeros(B, Hq, device="cuda")
+            self.ws = pkg.alloc_dense_workspace(B, Hq, H, d)
+
+        def step(self, stream=None):
+            x = self.x
+            pkg.page_plan(page, self.L, self.one, self.T, self.F, self.C, self.cu, self.slots, self.pos, err=self.err,
+                          stream=stream)
+            pkg.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + H], self.pos, self.q, q_weight=wq, k_weight=wk, v=x[:, Hq + H:],
+                             k_cache=self.kc, v_cache=self.vc, slot_map=self.slots, num_tokens=self.cu[B:], err=self.err,
+                             stream=stream)
+            pkg.dense_decode(self.q, self.K, self.V, self.L, self.out, self.ws, lse=self.lse, err=self.err, stream=stream)
+
+    a, b = State(), State()
+    side = torch.cuda.Stream()
+    warm = State()
+    warm.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step()
+    for x in xs:
+        a.x.copy_(x)
+        b.x.copy_(x)
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        b.step(side)
+        torch.cuda.current_stream().wait_stream(side)
+        for n in ("L", "T", "C", "cu", "slots", "pos", "q", "kc", "vc", "out", "lse"):
+            assert torch.equal(getattr(a, n), getattr(b, n)), n
+    torch.cuda.synchronize()
+    assert int(a.err) == 0 and a.L.tolist() == [n + steps for n in lens0]
+
+
+def test_two_streams_at_once():
+    """Two dense decodes and two gradient passes with workspaces of their own, overlapping on two streams."""
+    pkg, B, Hq, H, d, T = S(), 4, 8, 2, 128, 300
+    gn = gen(41)
+    rows = Rows(gn, B, H, 5000, d, 64, BF16, "head")
+    lens = i32([5000, 17, 3333, 1024])
+    x, w, pos = rnd(gn, T, Hq, d, dt=BF16), rnd(gn, d, dt=BF16), torch.arange(T, dtype=torch.int32, device="cuda")
+    qs, gs = [rnd(gn, B, Hq, d, dt=BF16) for _ in range(2)], [rnd(gn, T, Hq, d, dt=BF16) for _ in range(2)]
+
+    def work(i, stream=None):
+        out, dq, dw = torch.empty_like(qs[i]), torch.empty_like(gs[i]), torch.empty(d, device="cuda")
+        ws, wn = pkg.alloc_dense_workspace(B, Hq, H, d), pkg.alloc_norm_workspace(d)
+        torch.cuda.synchronize()
+
+        def go():
+            for _ in range(10):
+                pkg.dense_decode(qs[i], rows.kc, rows.vc, lens, out, ws, stream=stream)
+                pkg.qk_norm_rope_backward(gs[i], None, x, None, pos, dq, None, wn, w, None, dw, None, stream=stream)
+        return go, (out, dq, dw)
+
+    want = []
+    for i in range(2):
+        go, res = work(i)
+        go()
+        want.append(res)
+    torch.cuda.synchronize()
+    runs = [work(i, torch.cuda.Stream()) for i in range(2)]
+    for go, _ in runs:
+        go()
+    torch.cuda.synchronize()
+    for (_, got), ref in zip(runs, want):
+        for a, b in zip(got, ref):
+            assert torch.equal(a, b)
