@@ -27,5 +27,6 @@ __all__ = list(_PUBLIC)
 def __getattr__(name):
     if name in _PUBLIC:
         from . import seer
-        return getattr(seer, name)
+        value = globals()[name] = getattr(seer, name)   # once: this lookup costs as much as a call's launch
+        return value
     raise AttributeError(name)

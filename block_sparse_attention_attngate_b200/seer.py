@@ -665,7 +665,9 @@ def page_plan(page_size: int, seqlens: torch.Tensor, new_tokens: torch.Tensor, b
     positions int32 [room], filled with -1 / 0 behind the last token."""
     status = _call.page_plan(page_size, seqlens, new_tokens, block_table, free_list, free_count, cu_tokens, slot_map, positions,
                              seqlens_out, free_count_out, err, stream)
-    if status >= 0:
+    if status == 0:
+        return None
+    if status > 0:
         return _check(status)
     B = _page_args(page_size, seqlens, new_tokens, "new_tokens", block_table, free_list, free_count)
     seqlens_out = seqlens if seqlens_out is None else seqlens_out
@@ -695,7 +697,9 @@ def page_release(page_size: int, seqlens: torch.Tensor, finished: torch.Tensor, 
     seer_page_release); in place unless seqlens_out / free_count_out are given."""
     status = _call.page_release(page_size, seqlens, finished, block_table, free_list, free_count, seqlens_out, free_count_out,
                                 err, stream)
-    if status >= 0:
+    if status == 0:
+        return None
+    if status > 0:
         return _check(status)
     B = _page_args(page_size, seqlens, finished, "finished", block_table, free_list, free_count)
     seqlens_out = seqlens if seqlens_out is None else seqlens_out
@@ -808,7 +812,9 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions
     device) cuts the rows to the first so many.  rope_dim defaults to d."""
     status = _call.qk_norm_rope(q, k, positions, q_out, k_out, q_weight, k_weight, rope_base, rope_dim, eps, q_nope, k_nope, v,
                                 k_cache, v_cache, slot_map, num_tokens, err, stream)
-    if status >= 0:
+    if status == 0:
+        return None
+    if status > 0:
         return _check(status)
     shape, T, Hq, Hkv, d, dt = _qk_shape(q, k, rope_base, rope_dim, eps)
     rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
@@ -851,7 +857,9 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     None: that output had none.  workspace: alloc_norm_workspace(d), needed with norm weights."""
     status = _call.qk_norm_rope_backward(dq_out, dk_out, q, k, positions, dq, dk, workspace, q_weight, k_weight, dq_weight,
                                          dk_weight, rope_base, rope_dim, eps, dq_nope, dk_nope, num_tokens, stream)
-    if status >= 0:
+    if status == 0:
+        return None
+    if status > 0:
         return _check(status)
     shape, T, Hq, Hkv, d, dt = _qk_shape(q if q is not None else dq, k if k is not None else dk, rope_base, rope_dim, eps)
     rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
@@ -886,7 +894,9 @@ def dense_decode(q: torch.Tensor, k: KVCache, v: KVCache, seqlens: torch.Tensor,
     seer_dense_decode).  q and out [B, Hq, d]; k and v of the same type (bf16 or fp16), contiguous or paged with
     pages of any size."""
     status = _call.dense_decode(q, k._keep, v._keep, seqlens, out, workspace, window, softmax_scale, lse, err, stream)
-    if status >= 0:
+    if status == 0:
+        return None
+    if status > 0:
         return _check(status)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D [B, Hq, d] tensor")
