@@ -418,9 +418,12 @@ def spoil(rows, lens, window):
                 x[b, :, :lo] = math.inf
                 continue
             t = rows.table[b].long()
-            for at in list(range(0, lo)) + list(range(max(n, 0), len(t) * rows.page)):
-                if 0 <= int(t[at // rows.page]) < x.shape[0]:
-                    x[int(t[at // rows.page]), :, at % rows.page] = math.nan if at % 2 else -math.inf
+            at = torch.cat([torch.arange(0, lo), torch.arange(max(n, 0), len(t) * rows.page)]).cuda()
+            page = t[at // rows.page]
+            ok = (page >= 0) & (page < x.shape[0])
+            for odd, what in ((0, -math.inf), (1, math.nan)):
+                pick = ok & (at % 2 == odd)
+                x[page[pick], :, (at % rows.page)[pick]] = what
 
 
 def check_dense(B, g, H, d, lens, cap, page, dt, order, window=0, scale=0.0, bad=(), err_bits=0, seed=0, q_scale=1.0):
