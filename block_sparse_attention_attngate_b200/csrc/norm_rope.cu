@@ -10,9 +10,9 @@
 //   dy = R^T dz + dy',   dx = r (w dy) - x r^3 mean(w dy x),   dw = sum dy x r
 //
 // Bound: HBM -- every input is read once and every output written once.  Measured (graphs of the call, against the
-// copy bandwidth): 8192 tokens of 32 + 8 heads of 128, rotated and plain outputs and both caches in bf16, 51 us, 86 %
-// (the time does not move with the batch, the unit or the CTAs an SM); the gradients of the same rows 48 us, 80 %; 2049
-// tokens of 40 + 8 heads, half rotated, 11 us, 71 %.  The arithmetic is close behind the memory in the last two, so
+// copy bandwidth): 8192 tokens of 32 + 8 heads of 128, rotated and plain outputs and both caches in bf16, 48 us, 90 %;
+// the gradients of the same rows 48 us, 80 %; 2049
+// tokens of 40 + 8 heads, half rotated, 10 us, 77 %.  The arithmetic is close behind the memory in the last two, so
 // it is done two channels at a time (f32x2 instructions: 53 us against 50 without) and addresses are stepped.
 //
 // Layout.  D / 16 lanes share a row, two 8-channel chunks (16 bytes in 16-bit types) each:
@@ -214,12 +214,13 @@ __device__ __forceinline__ int cta_kind(const NormParams& p) {
   return k;
 }
 
-constexpr int kForwardBatch = 3;   // passes requested at once, in 16-bit types (4 spill: 11.9 us against 10.9 at odd sizes)
+// passes requested at once (three and four spill registers: 50.0 and 50.6 us against 48.4 for 8192 tokens)
+constexpr int kForwardBatch = 2;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kForwardCtas) norm_rope_kernel(const __grid_constant__ NormParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;   // lanes per row, rows per pass
-  constexpr int B = sizeof(T) == 4 ? 2 : kForwardBatch;
+  constexpr int B = kForwardBatch;
   __shared__ __align__(16) float angles[kWarps][2 * kMaxHalfGate];
   const int which = cta_kind(p);
   const NormKind& kd = p.kind[which];
