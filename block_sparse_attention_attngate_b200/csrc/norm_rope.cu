@@ -214,13 +214,15 @@ __device__ __forceinline__ int cta_kind(const NormParams& p) {
   return k;
 }
 
-// passes requested at once (three and four spill registers: 50.0 and 50.6 us against 48.4 for 8192 tokens)
-constexpr int kForwardBatch = 2;
+// passes requested at once (more spill registers: three 50.0 us, four 50.6 against 48.4 for 8192 tokens; two in fp32 53 against
+// 45 for 4096)
+template <typename T>
+constexpr int kForwardBatch = sizeof(T) == 4 ? 1 : 2;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kForwardCtas) norm_rope_kernel(const __grid_constant__ NormParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;   // lanes per row, rows per pass
-  constexpr int B = kForwardBatch;
+  constexpr int B = kForwardBatch<T>;
   __shared__ __align__(16) float angles[kWarps][2 * kMaxHalfGate];
   const int which = cta_kind(p);
   const NormKind& kd = p.kind[which];
