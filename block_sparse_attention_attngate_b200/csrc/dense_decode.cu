@@ -94,10 +94,27 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) { return pack_bf16(a, b); }
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+
+// A weight meets V as two numbers of the cache's type, its leading bits (cut, not rounded, so that the rest is not negative)
+// and the rest, each with a product of its own: 2^-15 (bf16) or 2^-21 (fp16) of it is lost.  One rounding loses up to 2^-8 or
+// 2^-11, as much as the output's own, and left the outputs a quarter to a third further from their 64-bit values.  The rest is
+// kept above zero: a value that is infinite and seen then gives infinity, not 0 x infinity.
+// fp16 has few exponents: its weights are 2^kLift times theirs (2^14 for the row's largest), with the sum, so that they
+// keep those bits down to 2^-18 of the largest and are good to 2^-37 of it below (unlifted, all below 2^-25 are lost, however
+// many they are).
+template <typename T>
+constexpr int kLift = std::is_same<T, __half>::value ? 14 : 0;
+
+__device__ __forceinline__ void split2(float a, float b, uint32_t& lead, uint32_t& rest, __nv_bfloat16) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  lead = __byte_perm(x, y, 0x7632);
+  rest = pack_bf16(fmaxf(a - __uint_as_float(x & 0xffff0000u), 1e-36f), fmaxf(b - __uint_as_float(y & 0xffff0000u), 1e-36f));
+}
+__device__ __forceinline__ void split2(float a, float b, uint32_t& lead, uint32_t& rest, __half) {
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(lead) : "f"(b), "f"(a));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lead));
+  const __half2 r = __floats2half2_rn(fmaxf(a - x.x, 0x1p-24f), fmaxf(b - x.y, 0x1p-24f));
+  rest = *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint16_t round1(float a, __nv_bfloat16) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(a));
@@ -187,7 +204,8 @@ __device__ __forceinline__ void finish(const DenseParams& p, size_t row0, int he
   uint16_t* out = p.out + (row0 + head) * D + k * 16 + quad;
   out[0] = round1(o.x * inv, T());
   out[8] = round1(o.y * inv, T());
-  if (p.lse && k == 0 && quad == 0) p.lse[row0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  if (p.lse && k == 0 && quad == 0)
+    p.lse[row0 + head] = l == 0.f ? -INFINITY : (m + (log2f(l) - kLift<T>)) * 0.6931471805599453f;
 }
 
 template <typename T, int D, int NT>
@@ -439,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
         }
 
         // running maximum, probabilities
-        uint32_t pt[MT][NT][2];
+        uint32_t pt[MT][NT][2], pr[MT][NT][2];   // leading bits, the rest
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float mx[2], al[2];
@@ -472,26 +490,39 @@ __global__ void __launch_bounds__(kThreads, 1) dense_decode_kernel(const __grid_
             float e[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float ref = m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1];   // nothing seen yet: 2^-inf = 0
+              const float ref = m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1] - kLift<T>;   // nothing seen yet: 2^-inf = 0
               e[j] = exp2f(s[i][n][j] - ref);
               l[n][j & 1] += e[j];
             }
-            pt[i][n][0] = transpose8x8(pack2(e[0], e[1], T()));
-            pt[i][n][1] = transpose8x8(pack2(e[2], e[3], T()));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              split2(e[2 * j], e[2 * j + 1], pt[i][n][j], pr[i][n][j], T());
+              pt[i][n][j] = transpose8x8(pt[i][n][j]);
+              pr[i][n][j] = transpose8x8(pr[i][n][j]);
+            }
           }
         }
 
-        // O^T += V^T P^T
+        // O^T += V^T P^T, two channel steps at a time: the two products of one do not wait for each other
         const uint32_t vb = next_slot();
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const int r = i * 16 + (lane & 7) + ((lane >> 4) << 3), ch = 2 * k + ((lane >> 3) & 1);
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4_trans(vb + r * (2 * D) + ((ch ^ (r & 7)) << 4), a0, a1, a2, a3);
+          for (int k = 0; k < KS; k += 2) {
+            const int r = i * 16 + (lane & 7) + ((lane >> 4) << 3);
+            uint32_t a[2][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma(o[n][k], a0, a1, a2, a3, pt[i][n][0], pt[i][n][1], T());
+            for (int u = 0; u < 2; ++u) {
+              const int ch = 2 * (k + u) + ((lane >> 3) & 1);
+              ldsm_x4_trans(vb + r * (2 * D) + ((ch ^ (r & 7)) << 4), a[u][0], a[u][1], a[u][2], a[u][3]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) mma(o[n][k + u], a[u][0], a[u][1], a[u][2], a[u][3], pt[i][n][0], pt[i][n][1], T());
+#pragma unroll
+              for (int u = 0; u < 2; ++u) mma(o[n][k + u], a[u][0], a[u][1], a[u][2], a[u][3], pr[i][n][0], pr[i][n][1], T());
+            }
           }
 
         ++step;

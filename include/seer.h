@@ -596,7 +596,8 @@ typedef struct {
  *   out[b, i] = sum_t softmax_t(scale * q[b, i] . K[b, h, t]) V[b, h, t]
  *   lse_out[b, i] = log sum_t exp(scale * q[b, i] . K[b, h, t])
  * L_b <= 0: out = 0, lse = -inf.  Scores, the running maximum and sum and the output are fp32; the
- * probabilities that weigh V are rounded to the cache's type (the sum is not).  A sequence longer than
+ * probabilities that weigh V lose at most 2^-15 (bf16) or 2^-21 (fp16; and 2^-37 of the row's largest) of
+ * themselves.  A sequence longer than
  * its cache (num_tokens, or max_pages_per_seq * page_size) is cut to it and sets SEER_DEVERR_COUNT; a
  * page id outside the pool leaves its tokens out and sets SEER_DEVERR_PAGE_INDEX.  Rows at or past
  * L_b and before the window are not used (they may hold anything, NaN included).
