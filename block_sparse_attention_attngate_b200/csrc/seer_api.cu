@@ -887,12 +887,16 @@ extern "C" {
 
 namespace {
 
+// The page kernels count in 32 bits and step past the last element by up to a grid's threads (64 x 1024) before they stop.
+constexpr int32_t kMaxPageItems = INT32_MAX - (1 << 17) + 1;   // 2^31 - 2^17
+
 seer_status check_pages(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq) {
   if (batch < 1 || page_size < 1 || num_pages < 1 || max_pages_per_seq < 1)
     return fail(SEER_ERR_INVALID_ARG, "batch, page_size, num_pages and max_pages_per_seq must be >= 1");
   if (batch > seer::kMaxDecodeB) return fail(SEER_ERR_UNSUPPORTED, "batch %d > %d", batch, seer::kMaxDecodeB);
   if ((int64_t)num_pages * page_size > INT32_MAX)
     return fail(SEER_ERR_UNSUPPORTED, "num_pages * page_size must be below 2^31");
+  if (num_pages > kMaxPageItems) return fail(SEER_ERR_UNSUPPORTED, "num_pages %d above 2^31 - 2^17", num_pages);
   return SEER_OK;
 }
 
@@ -908,6 +912,7 @@ seer_status seer_page_plan(int32_t batch, int32_t page_size, int32_t num_pages, 
   seer_status st = check_pages(batch, page_size, num_pages, max_pages_per_seq);
   if (st != SEER_OK) return st;
   if (max_tokens < 1) return fail(SEER_ERR_INVALID_ARG, "max_tokens must be >= 1");
+  if (max_tokens > kMaxPageItems) return fail(SEER_ERR_UNSUPPORTED, "max_tokens %d above 2^31 - 2^17", max_tokens);
   const void* const ptrs[] = {seqlens,     new_tokens,     block_table, free_list, free_count,
                               seqlens_out, free_count_out, cu_tokens,   slot_map,  positions};
   for (const void* p : ptrs) {

@@ -456,9 +456,10 @@ typedef enum { SEER_BF16 = 0, SEER_FP16 = 1, SEER_FP32 = 2 } seer_dtype;
  *   cu_tokens                   device int32 [B + 1]
  *   slot_map, positions         device int32 [max_tokens]
  *   err_word                    device int32 or NULL
- * batch <= 4096; num_pages * page_size < 2^31; a length of 2^31 or more after the call counts as too
- * many pages.  Integers need no 16-byte alignment (4 bytes do).  Other buffers must not overlap.  One
- * launch, of one CTA or of several when there is much to write.
+ * batch <= 4096; num_pages * page_size < 2^31; max_tokens and num_pages at most 2^31 - 2^17 (num_pages in
+ * seer_page_release too); a length of 2^31 or more after the call counts as too many pages.  Integers need
+ * no 16-byte alignment (4 bytes do).  Other buffers must not overlap.  One launch, of one CTA or of several
+ * when there is much to write.
  */
 seer_status seer_page_plan(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
                            int32_t max_tokens, const int32_t* seqlens, const int32_t* new_tokens,
