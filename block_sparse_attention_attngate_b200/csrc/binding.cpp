@@ -112,7 +112,7 @@ struct Call {
   }
   int32_t i32(PyObject* o) {
     const long v = PyLong_Check(o) ? PyLong_AsLong(o) : (ok = false, 0);
-    if (v > INT32_MAX || v < INT32_MIN) ok = false;
+    if (v > INT32_MAX || v < INT32_MIN || (v == -1 && PyErr_Occurred())) ok = false;   // the error: beyond 64 bits
     return (int32_t)v;
   }
   float f32(PyObject* o) {

@@ -182,6 +182,17 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _i32(x, name: str) -> int:
+    """x as a 32-bit argument of a C call (ctypes would take a larger number modulo 2^32, int() the floor of a fraction)."""
+    try:
+        n = int(x)
+    except (OverflowError, ValueError):   # infinity, NaN
+        n = None
+    if n is None or n != x or not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must be a whole number of 32 bits, got {x}")
+    return n
+
+
 def _need_shape(t, shape, name: str):
     """The kernels index these buffers by the problem shape: a smaller tensor would be written past."""
     if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(int(x) for x in shape):
@@ -677,6 +688,7 @@ def page_plan(page_size: int, seqlens: torch.Tensor, new_tokens: torch.Tensor, b
     _need_shape(cu_tokens, (B + 1,), "cu_tokens")
     if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1 or slot_map.numel() < 1:
         raise ValueError("slot_map must be a 1-D tensor of at least one slot")
+    _i32(slot_map.numel(), "slot_map's length")
     _need_shape(positions, slot_map.shape, "positions")
     _need_err(err)
     for t, name in ((seqlens, "seqlens"), (new_tokens, "new_tokens"), (block_table, "block_table"),
@@ -717,14 +729,17 @@ def page_release(page_size: int, seqlens: torch.Tensor, finished: torch.Tensor, 
 
 
 def _page_args(page_size, seqlens, per_request, name: str, block_table, free_list, free_count) -> int:
+    _i32(page_size, "page_size")
     if not isinstance(seqlens, torch.Tensor) or seqlens.dim() != 1:
         raise ValueError("seqlens must be a 1-D tensor")
-    B = int(seqlens.shape[0])
+    B = _i32(seqlens.shape[0], "seqlens' length")
     _need_shape(per_request, (B,), name)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, pages)")
     if not isinstance(free_list, torch.Tensor) or free_list.dim() != 1:
         raise ValueError("free_list must be a 1-D tensor of num_pages entries")
+    _i32(block_table.shape[1], "block_table's width")
+    _i32(free_list.numel(), "free_list's length")
     _need_shape(free_count, (1,), "free_count")
     return B
 
@@ -752,10 +767,11 @@ def _pool(t: Optional[torch.Tensor], heads: int, d: int, dtype: torch.dtype, nam
     if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[1] != heads or t.shape[3] != d:
         got = tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name} must be a [pages, {heads}, page, {d}] view, got {got}")
+    page = _i32(t.shape[2], f"{name}'s page")
     _need(t, dtype, name, contiguous=False)
     if t.stride(3) != 1:
         raise ValueError(f"{name} must have unit-stride channels")
-    pages, page = t.shape[0], t.shape[2]
+    pages = t.shape[0]
     st = t.stride(2) if page > 1 else d
     sh = t.stride(1) if heads > 1 else st * page
     return PoolDesc(t.data_ptr(), t.stride(0) if pages > 1 else sh * heads, sh, st, pages, page)
@@ -771,10 +787,10 @@ def _qk_shape(q, k, rope_base: float, rope_dim: Optional[int], eps: float):
         raise ValueError("q or k is needed")
     if one.dtype not in DTYPES:
         raise TypeError(f"q and k must be one of {list(DTYPES)}, got {one.dtype}")
-    T, d = int(one.shape[0]), int(one.shape[2])
-    Hq = int(q.shape[1]) if q is not None else int(k.shape[1])
-    Hkv = int(k.shape[1]) if k is not None else Hq
-    rope = d if rope_dim is None else int(rope_dim)
+    T, d = _i32(one.shape[0], "the number of tokens"), _i32(one.shape[2], "the head dimension")
+    Hq = _i32(one.shape[1], "the number of heads")
+    Hkv = _i32(k.shape[1], "the number of heads") if k is not None else Hq
+    rope = d if rope_dim is None else _i32(rope_dim, "rope_dim")
     return QkShape(T, Hq, Hkv, d, rope, DTYPES[one.dtype], float(rope_base), float(eps)), T, Hq, Hkv, d, one.dtype
 
 
@@ -817,10 +833,10 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions
     if status > 0:
         return _check(status)
     shape, T, Hq, Hkv, d, dt = _qk_shape(q, k, rope_base, rope_dim, eps)
+    pools = [_pool(t, Hkv, d, dt, name) for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"))]
     rows = [_rows(t, T, h, d, dt, name) for t, h, name in (
         (q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"), (q_out, Hq, "q_out"), (k_out, Hkv, "k_out"),
         (q_nope, Hq, "q_nope"), (k_nope, Hkv, "k_nope"))]
-    pools = [_pool(t, Hkv, d, dt, name) for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache"))]
     _norm_vectors(((q_weight, "q_weight"), (k_weight, "k_weight")), d, dt)
     _token_args(positions, num_tokens, T, shape.rope_dim > 0)
     if slot_map is not None:
@@ -836,7 +852,7 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions
 
 
 def norm_workspace_bytes(head_dim: int) -> int:
-    return int(_lib.seer_qk_norm_rope_workspace_bytes(int(head_dim)))
+    return int(_lib.seer_qk_norm_rope_workspace_bytes(_i32(head_dim, "head_dim")))
 
 
 def alloc_norm_workspace(head_dim: int, device=None) -> torch.Tensor:
@@ -877,7 +893,8 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
 
 
 def dense_decode_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    shape = DenseShape(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), 0, 1, 0, 0.0)
+    shape = DenseShape(_i32(batch, "batch"), _i32(num_q_heads, "num_q_heads"), _i32(num_kv_heads, "num_kv_heads"),
+                       _i32(head_dim, "head_dim"), 0, 1, 0, 0.0)
     return int(_lib.seer_dense_decode_workspace_bytes(ctypes.byref(shape)))
 
 
@@ -900,7 +917,8 @@ def dense_decode(q: torch.Tensor, k: KVCache, v: KVCache, seqlens: torch.Tensor,
         return _check(status)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D [B, Hq, d] tensor")
-    B, Hq, d = (int(x) for x in q.shape)
+    _i32(window, "window")
+    B, Hq, d = (_i32(x, "an extent of q") for x in q.shape)
     heads, pages = [], []
     for c, name in ((k, "k"), (v, "v")):
         t = c._keep[0]
@@ -908,10 +926,10 @@ def dense_decode(q: torch.Tensor, k: KVCache, v: KVCache, seqlens: torch.Tensor,
             raise ValueError(f"{name}: rows of {d} channels are needed, got {tuple(t.shape)}")
         if c.dtype != q.dtype:
             raise TypeError(f"{name} must be {q.dtype}, got {c.dtype}")
-        heads.append(int(t.shape[1]))
+        heads.append(_i32(t.shape[1], f"{name}'s number of heads"))
         if c.desc.layout == KV_PAGED:
-            pages.append(int(t.shape[2]))
-            if c._keep[1].dim() != 2 or c._keep[1].shape[0] < B:
+            pages.append(_i32(t.shape[2], f"{name}'s page"))
+            if c._keep[1].dim() != 2 or c._keep[1].shape[0] < B or c._keep[1].shape[1] >= 2 ** 31:
                 raise ValueError(f"{name}: a block table of {B} rows is needed, got {tuple(c._keep[1].shape)}")
         elif t.shape[0] < B:
             raise ValueError(f"{name}: a cache of {B} sequences is needed, got {tuple(t.shape)}")
