@@ -18,6 +18,8 @@ from typing import Optional
 
 import torch
 
+from .build import call_layer_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # SEER_LIBRARY selects another build of the library (e.g. a variant with different tile choices)
 LIB_PATH = os.environ.get("SEER_LIBRARY") or os.path.join(_HERE, "libseer.so")
@@ -145,7 +147,7 @@ class _NoCallLayer:
 def _load_call_layer():
     """The compiled call layer of the operators around the decode step, bound to the loaded library.  Nothing but time
     depends on it, so the package works without one that loads, and says so."""
-    path = os.path.join(_HERE, "_seer_call.so")
+    path = call_layer_path()
     try:
         if not os.path.exists(path):
             raise ImportError(f"{path} is missing")

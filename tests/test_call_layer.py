@@ -59,3 +59,31 @@ def test_package_without_the_call_layer(tmp_path, broken):
 def test_the_call_layer_is_loaded_here():
     assert set(seer._call.entries()) == {"seer_page_plan", "seer_page_release", "seer_qk_norm_rope", "seer_qk_norm_rope_backward",
                                          "seer_dense_decode"}
+
+
+# ---------------------------------------------------------------- building it
+from block_sparse_attention_attngate_b200 import build as B   # noqa: E402
+
+
+def test_a_layer_of_another_torch_is_not_used(monkeypatch):
+    """The layer is compiled against one Python and one torch; both are in its name, so another's is neither taken for
+    up to date nor loaded."""
+    import torch
+    here = B.call_layer_path()
+    assert os.path.exists(here) and seer._call.__spec__.origin == here
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert B.call_layer_path() != here
+    with pytest.warns(RuntimeWarning, match="call layer"):
+        assert isinstance(seer._load_call_layer(), seer._NoCallLayer)
+    monkeypatch.undo()
+    monkeypatch.setattr(sys.implementation, "cache_tag", "other-11")
+    assert B.call_layer_path() != here
+
+
+def test_the_library_is_built_without_the_call_layer(monkeypatch):
+    """No compiler for the layer, or no torch: the library is there all the same, and a warning tells of the layer."""
+    def fails(*a, **k):
+        raise RuntimeError("no g++")
+    monkeypatch.setattr(B, "build_call_layer", fails)
+    with pytest.warns(RuntimeWarning, match="no g[+][+]"):
+        assert B.build() == B.LIB and os.path.exists(B.LIB)
