@@ -373,6 +373,7 @@ PyObject* dense_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.page_size = page ? (int32_t)page : 1;
     s.window = c.i32(a[6]);
     s.softmax_scale = c.f32(a[7]);
+    if (s.softmax_scale == 0.f && PyObject_IsTrue(a[7]) == 1) return -1;   // not 0 but for its rounding
     const void* qp = c.dense(a[0], {B, Hq, d}, type);
     const auto* lens = static_cast<int32_t*>(c.dense(a[3], {B}, kI32));
     void* out = c.dense(a[4], {B, Hq, d}, type);

@@ -936,6 +936,8 @@ def dense_decode(q: torch.Tensor, k: KVCache, v: KVCache, seqlens: torch.Tensor,
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D [B, Hq, d] tensor")
     _i32(window, "window")
+    if softmax_scale != 0 and ctypes.c_float(float(softmax_scale)).value == 0:
+        raise ValueError(f"softmax_scale {softmax_scale} is 0 in fp32, which asks for 1 / sqrt(head_dim)")
     B, Hq, d = (_i32(x, "an extent of q") for x in q.shape)
     heads, pages = [], []
     for c, name in ((k, "k"), (v, "v")):

@@ -93,3 +93,13 @@ def test_workspace_sizes_of_numbers_past_32_bits():
     for name in good:
         with pytest.raises(ValueError, match=name):
             S.dense_decode_workspace_bytes(**{**good, name: good[name] + 2 ** 32})
+
+
+def test_softmax_scale_below_fp32_is_refused():
+    """Rounded to fp32 it would be 0, which asks for 1 / sqrt(head_dim)."""
+    for bad in (1e-46, -1e-300):
+        with pytest.raises(ValueError, match="softmax_scale"):
+            S.dense_decode(**DENSE, softmax_scale=bad)
+    for fine in (0, 0.0, 2e-45, 1, 0.125):
+        with pytest.raises(TypeError, match="CUDA tensor"):
+            S.dense_decode(**DENSE, softmax_scale=fine)
