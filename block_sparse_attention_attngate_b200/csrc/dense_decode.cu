@@ -7,11 +7,16 @@
 //   m' = max(m, max s),  o' = o 2^(m - m') + sum 2^(s - m') V,  l' likewise,
 // and pieces (m_i, l_i, o_i) of one row join by the same rule.
 //
-// Bound: HBM -- every key and value is read once; 4 g flops a byte pair at most, a
-// tenth of what the warp-level tensor instructions sustain (measured, graphs of the call, of the copy
-// bandwidth: 4 x 65536 tokens, 8 KV heads of 128, four query heads each, pages of 64, bf16: 170 us, 96 %; 16
-// sequences of 8000 to 32000 tokens, five heads, token-major pages of 16, fp16: 198 us, 101 %; 16 heads: 85 %; one sequence
-// of 2048 tokens, one KV head: 8.5 us, all of it latency: lengths, page ids, rows, the merge, the join's two round trips).
+// Bound: HBM -- every key and value is read once; three products of g heads a key, 15 % of what the warp-level tensor
+// instructions sustain (measured with inputs that change from call to call, against the copy bandwidth: 4 x 65536
+// tokens, 8 KV heads of 128, four query heads each, pages of 64, bf16: 167 to 171 us, 96 to 98 %; 16 sequences of 8000 to 32000
+// tokens, five heads, token-major pages of 16, fp16: 204 to 209 us, 93 to 95 %; 8 x 32768 tokens, 4 KV heads of 128, 16 heads each:
+// 101 us, 81 %; one sequence of 2048 tokens, one KV head: 8.6 us, all of it latency: lengths, page ids, rows, the merge, the join's
+// two round trips).  Rows of some hundred tokens are two to three times as long as their bytes: 8 x 1000 tokens 16.4 us (floor 5.0),
+// 64 x 300 25 us (12.0), one row of 32768 beside 63 of 20 51 us (21.3).
+//
+// The figures of the choices below are of graphs that repeat one call, with the weights of one rounding (below); inputs under
+// 126 MB then lie in L2, and a call with others takes 10 to 15 % more.
 //
 // Split.  The rows' (sequence, KV head) tokens in units of kDenseUnit are one long axis; equal ranges of it are the work
 // of as many teams, one wave.  A team's warps take its steps of 4 KB of keys and 4 KB of values in turn, each through a ring
@@ -48,11 +53,16 @@ namespace {
 
 constexpr int kWarps = 12, kSlots = 3;   // of a CTA, of a warp's ring
 constexpr int kThreads = kWarps * 32;
-constexpr int kTeamRows = 6;       // rows an SM from which on teams are single warps whatever the lengths
+// Rows an SM from which on teams are single warps whatever the lengths.  A long row among so many then lies in hundreds of ranges,
+// which the join takes one after another: 128 sequences of 20 tokens, one of them 20000, 8 KV heads of 128: 73 us, floor 14.
+constexpr int kTeamRows = 6;
 constexpr int kTeamUnits = 24;     // units of the mean token's row from which on teams are CTAs (1000 tokens: 22 us against 29)
 constexpr int kPad = 6;
 constexpr int kMinUnits = 4, kMinUnitsTeam = 8;   // of a range, about (warps: 64 short sequences 24 us, 31 us with eight)
-constexpr int kWholeUnits = 24;    // rows up to this, padding included, are not split: a join takes 2.4 us (100 tokens: 6.5 us against 8.8)
+// While the mean row, padding included, is no longer than this there are as many ranges as rows, if there are teams for them: equally
+// long rows then lie in one range each and need no join, which takes 2.4 us (100 tokens: 6.5 us against 8.8).  Ranges are equal,
+// so rows of different lengths are still cut where the ranges end.
+constexpr int kWholeUnits = 24;
 constexpr int kSlotBytes = 4096;   // keys or values of one step
 constexpr int kMaskSteps = 4;      // steps whose masks are kept: more than are in the ring
 static_assert(kMaskSteps > (kSlots + 1) / 2, "a mask outlives its step");

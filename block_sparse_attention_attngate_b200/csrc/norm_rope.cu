@@ -9,11 +9,13 @@
 // Backward, with r = 1 / sqrt(mean(x^2) + eps):
 //   dy = R^T dz + dy',   dx = r (w dy) - x r^3 mean(w dy x),   dw = sum dy x r
 //
-// Bound: HBM -- every input is read once and every output written once.  Measured (graphs of the call, against the
-// copy bandwidth): 8192 tokens of 32 + 8 heads of 128, rotated and plain outputs and both caches in bf16, 48 us, 90 %;
-// the gradients of the same rows 48 us, 80 %; 2049
-// tokens of 40 + 8 heads, half rotated, 10 us, 77 %.  The arithmetic is close behind the memory in the last two, so
-// it is done two channels at a time (f32x2 instructions: 53 us against 50 without) and addresses are stepped.
+// Bound: HBM -- every input is read once and every output written once.  Measured (inputs that change from call to call,
+// against the copy bandwidth): 8192 tokens of 32 + 8 heads of 128, rotated and plain outputs and both caches in bf16, 49 to
+// 50 us, 87 to 89 %; the gradients of the same rows 49 to 51 us, 75 to 79 %, with those of the un-rotated rows 77 us, 67 %; 4096
+// tokens in fp32 33 us, 78 %, their gradients 75 us, 51 % (two stages in the ring: a pass waits for the newest request); 2049
+// tokens of 40 + 8 heads in fp16, half rotated, 13.1 us, 59 % (9.9 us where the inputs lie in L2).  The arithmetic is close
+// behind the memory in the gradients, so it is done two channels at a time (f32x2 instructions: 50 us, 53 without) and addresses
+// are stepped.
 //
 // Layout.  D / 16 lanes share a row, two 8-channel chunks (16 bytes in 16-bit types) each:
 // lane l of a row takes chunks l and l + rope_dim / 16 while those are
@@ -370,7 +372,9 @@ template <typename T>
 constexpr int backward_stages() { return sizeof(T) == 4 ? 2 : 4; }
 
 // Backward: the weight gradient of a lane's 16 channels stays in registers over the warp's passes; at the end the lanes
-// and warps of the CTA are added up in a fixed order and go to the CTA's row of the workspace.
+// and warps of the CTA are added up in a fixed order and go to the CTA's row of the workspace.  These sums are fp32, as
+// sine and cosine are (of angles reduced in fp64): chains are short (8 passes for most sizes, 32 lanes, up to 32 CTAs a thread), and
+// fp32 gradients come out 2e-7 from their 64-bit values, where sums and angles in 64 bits leave 8e-8.
 // Y: whether the un-rotated rows have a gradient.
 template <typename T, int D, bool Y>
 __global__ void __launch_bounds__(kThreads, kBackwardCtas) norm_rope_backward_kernel(const __grid_constant__ NormParams p) {

@@ -478,7 +478,8 @@ seer_status seer_page_plan(int32_t batch, int32_t page_size, int32_t num_pages, 
  * max_pages_per_seq pages of a finished request, F outside [0, num_pages], or more than num_pages
  * free pages afterwards: SEER_DEVERR_COUNT and nothing changes).  A page id outside [0, num_pages) is
  * pushed as -1 and sets SEER_DEVERR_PAGE_INDEX.  A request released twice without a plan in between
- * has length 0 the second time and gives nothing back.
+ * has length 0 the second time and gives nothing back.  Pages have no reference counts: one that several finished
+ * requests list is pushed once for each of them, and one that an unfinished request lists too is pushed all the same.
  *   seqlens_out, free_count_out may be seqlens / free_count themselves.
  */
 seer_status seer_page_release(int32_t batch, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
