@@ -108,7 +108,8 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 // A weight meets V as two numbers of the cache's type, its leading bits (cut, not rounded, so that the rest is not negative)
 // and the rest, each with a product of its own: 2^-15 (bf16) or 2^-21 (fp16) of it is lost.  One rounding loses up to 2^-8 or
 // 2^-11, as much as the output's own, and left the outputs a quarter to a third further from their 64-bit values.  The rest is
-// kept above zero: a value that is infinite and seen then gives infinity, not 0 x infinity.
+// kept above zero: a value that is infinite and seen then gives infinity, not 0 x infinity (while its weight's leading bits are
+// not 0: fp16 down to 2^-38 of the largest).
 // fp16 has few exponents: its weights are 2^kLift times theirs (2^14 for the row's largest), with the sum, so that they
 // keep those bits down to 2^-18 of the largest and are good to 2^-37 of it below (unlifted, all below 2^-25 are lost, however
 // many they are).
